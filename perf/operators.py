@@ -71,7 +71,10 @@ def draw(rng):
             c["D"] = _spread(rng, 1, 128)
             c["mask"] = rng.choice(["both", "causal", "window"])
             c["NB"] = _spread(rng, 4, 40)
-        if 0.0005 * most[op] <= _cost(c) <= most[op]:
+        # a row of dS sums to zero: where every row sees one bucket alone, the table's gradient is 0 and has no
+        # size that an error could be compared with
+        one_bucket = op == "train" and (c["T"] < 2 or c["mask"] == "window" and c["D"] < 4)
+        if 0.0005 * most[op] <= _cost(c) <= most[op] and not one_bucket:
             return c
 
 
@@ -304,9 +307,11 @@ def run(state):
             out, lse = fps.skiparse2d_attn_relbias_fwd(s["q"], s["k"], s["v"], s["table"], s["buckets"], c["P"], c["mode"])
             return {"out": out, "lse": lse}
         if c["op"] == "train":
-            out, lse = fps.skiparse2d_attn_relbias_fwd(s["q"], s["k"], s["v"], s["table"], s["buckets"], c["P"], c["mode"])
+            out_lo = torch.empty_like(s["q"])  # what rounding took from out
+            out, lse = fps.skiparse2d_attn_relbias_fwd(s["q"], s["k"], s["v"], s["table"], s["buckets"], c["P"], c["mode"],
+                                                       out_lo=out_lo)
             dq, dk, dv, dtable = fps.skiparse2d_attn_relbias_bwd(s["q"], s["k"], s["v"], out, s["dout"], lse, s["table"],
-                                                                 s["buckets"], c["P"], c["mode"])
+                                                                 s["buckets"], c["P"], c["mode"], out_lo=out_lo)
             return {"out": out, "dq": dq, "dk": dk, "dv": dv, "dtable": dtable}
         cache = fps.FrameCache(s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
         if c["op"] == "append":
