@@ -12,6 +12,10 @@ from __future__ import annotations
 import torch
 
 from ._lib import STATUS, SkiparseError, check, lib
+from .frames import (FrameCache, SkiparseRelBiasAttention, frame_buckets, frame_cache, skiparse1d_attn_cached,
+                     skiparse1d_attn_relbias_bwd, skiparse1d_attn_relbias_fwd, skiparse1d_cache_append,
+                     skiparse2d_attn_cached, skiparse2d_attn_relbias_bwd, skiparse2d_attn_relbias_fwd,
+                     skiparse2d_cache_append)
 
 TOKEN_WISE = 0
 GROUP_WISE = 1
@@ -22,7 +26,10 @@ __all__ = ["TOKEN_WISE", "GROUP_WISE", "SkiparseError", "skiparse2d_attn_fwd", "
            "skiparse2d_attn_fwd_lse", "skiparse2d_attn_bwd", "SkiparseAttention", "skiparse_attention",
            "skiparse1d_attn_fwd", "skiparse1d_attn_fwd_lse", "skiparse1d_attn_bwd", "skiparse1d_rearrange",
            "skiparse1d_unrearrange", "skiparse1d_switch_mode", "padded_length_1d", "attn_fwd_host",
-           "host_workspace_bytes"]
+           "host_workspace_bytes", "FrameCache", "SkiparseRelBiasAttention", "frame_buckets", "frame_cache",
+           "skiparse2d_attn_relbias_fwd", "skiparse2d_attn_relbias_bwd", "skiparse2d_cache_append",
+           "skiparse2d_attn_cached", "skiparse1d_attn_relbias_fwd", "skiparse1d_attn_relbias_bwd",
+           "skiparse1d_cache_append", "skiparse1d_attn_cached"]
 
 
 def _stream_ptr(stream) -> int:
@@ -204,8 +211,14 @@ class SkiparseAttention(torch.autograd.Function):
         return dq, dk, dv, None, None, None
 
 
-def skiparse_attention(q, k, v, P: int, mode: int, dims: int = 2):
-    """Autograd-aware Skiparse attention on (B,T,H,W,heads,d) bf16 CUDA tensors."""
+def skiparse_attention(q, k, v, P: int, mode: int, dims: int = 2, table=None, buckets=None):
+    """Autograd-aware Skiparse attention on (B,T,H,W,heads,d) bf16 CUDA tensors. With `table`
+    (num_buckets, heads) bf16 and `buckets` (frame_buckets), scores get the learned bias by frame
+    distance and its masks (skiparse2d_attn_relbias_fwd), and the table its gradient."""
+    if (table is None) != (buckets is None):
+        raise ValueError("table and buckets belong together")
+    if table is not None:
+        return SkiparseRelBiasAttention.apply(q, k, v, table, buckets, P, mode, dims)
     return SkiparseAttention.apply(q, k, v, P, mode, dims)
 
 

@@ -53,6 +53,16 @@ SIGNATURES = {
     "skiparse1d_attn_fwd_host": (_I, [_VP] * 4 + [_I] * 9 + [_VP, ctypes.c_size_t, _VP]),
     "skiparse_attn_fwd_host_workspace_bytes": (_LL, [_I] * 7),
 }
+for _n in ("1d", "2d"):  # the frame-aware operators
+    SIGNATURES.update({
+        f"skiparse{_n}_attn_relbias_fwd": (_I, [_VP] * 5 + [_I] * 2 + [_VP] * 3 + [_I] * 8 + [_VP]),
+        f"skiparse{_n}_attn_relbias_bwd": (_I, [_VP] * 9 + [_I] * 2 + [_VP] * 5 + [ctypes.c_size_t] + [_I] * 8 + [_VP]),
+        f"skiparse{_n}_attn_relbias_bwd_workspace_bytes": (_LL, [_I] * 8),
+        f"skiparse{_n}_cache_append": (_I, [_VP] * 7 + [_I] * 9 + [_VP]),
+        f"skiparse{_n}_cache_frame_tokens": (_LL, [_I] * 3),
+        f"skiparse{_n}_attn_cached": (_I, [_VP] * 8 + [_I] * 2 + [_VP] * 3 + [ctypes.c_size_t] + [_I] * 9 + [_VP]),
+        f"skiparse{_n}_attn_cached_workspace_bytes": (_LL, [_I] * 8),
+    })
 
 STATUS = {0: "SKIPARSE_OK", 1: "SKIPARSE_ERR_INVALID_ARG", 2: "SKIPARSE_ERR_UNSUPPORTED",
           3: "SKIPARSE_ERR_MISALIGNED", 4: "SKIPARSE_ERR_CUDA", 5: "SKIPARSE_ERR_TIMEOUT",

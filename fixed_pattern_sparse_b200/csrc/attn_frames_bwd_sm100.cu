@@ -1,0 +1,700 @@
+// attn_frames_bwd_sm100.cu -- backward pass of the class attention with a learned bias by frame
+// distance (sm_100a).
+//
+// For one (b, class, head) subsequence, with P = exp(s - L) recomputed from the biased, masked
+// scores s = q.k/sqrt(d) + bias[t_q - t_k] and the forward's log-sum-exp L, and D_i = dO_i . O_i:
+//   dV = P^T dO,  dP = dO V^T,  dS = P o (dP - D),  dQ = dS K / sqrt(d),  dK = dS^T Q / sqrt(d),
+//   dtable[g][head] = sum of dS_ij over all pairs (i, j) whose distance lies in bucket g.
+// The schedule is that of the unbiased backward pass (attn_bwd_sm100.cu): a key-major kernel for dK
+// and dV and a query-major one for dQ, seven tile products per pair of tiles, no atomics on
+// results. What the bias adds:
+//   * Frames. Within 64 columns of one frame the bias is one number per row: in the query-major
+//     kernel it joins the row's log-sum-exp in the existing FMA (no instruction per score), in
+//     the key-major one it is added to each column's. Columns of several frames look the bias up
+//     where the frame changes. Streamed tiles that no stationary row can see are skipped.
+//   * D. Every row of dS sums to zero over its keys, so an error of D_i enters the bias gradient
+//     through all of the row's keys with one sign. D from the bf16 output would dominate that
+//     gradient's error; the forward can therefore store what rounding its output took (out_lo).
+//   * Bias gradient. The key-major kernel sums dS, in fp32, before its rounding to bf16, in a
+//     register per key row for as long as the streamed queries stay in one frame; when the
+//     frame changes, the warp adds its rows of equal distance by shuffles and one lane adds the
+//     sum to the warp's own table of distances in shared memory. A CTA writes the sum of its
+//     eight tables, in a fixed order, to the workspace, and the last kernel adds those rows and
+//     joins distances to buckets, in a fixed order too: the result does not depend on timing.
+//     Per score this costs one addition (half of one packed instruction).
+// Launches: row statistics (D, L in log2, the bias by head and distance), dK/dV, dQ, dtable.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "frames_common.cuh"
+
+namespace skiparse {
+namespace {
+
+// 13 warps: softmax 0-7, producers 8-11 (warps 8-9 copy the first streamed tensor and the
+// statistics, warps 10-11 the second, each pair splitting a tile's rows), MMA issuer 12.
+constexpr int kBwdThreads = 416;
+constexpr int kBwdProd0 = 8;
+constexpr int kBwdProducers = 128;
+constexpr int kBwdMma = 12;
+constexpr int kBwdSoftmax = 256;
+constexpr int kMaxSmem = 232448;  // 227 KB, the most a CTA may have
+
+template <int D, bool KV>
+struct BwdCfg : TileGeom<D> {
+    using G = TileGeom<D>;
+    using G::TILE_BYTES;
+    // ring slots of the two streamed tensors: B1 = Q (key-major) or K (query-major), B2 = dO or V
+    static constexpr int NS1 = KV ? 2 : 3, NS2 = 2;
+    static constexpr int OFF_A1 = 0;
+    static constexpr int OFF_A2 = TILE_BYTES;
+    static constexpr int OFF_B1 = 2 * TILE_BYTES;
+    static constexpr int OFF_B2 = OFF_B1 + NS1 * TILE_BYTES;
+    static constexpr int OFF_VEC = OFF_B2 + NS2 * TILE_BYTES;  // [B1 slot or stationary][L,D][128] fp32
+    static constexpr int VEC_BYTES = (KV ? NS1 : 1) * 2 * kTileRows * 4;
+    static constexpr int OFF_HIST = OFF_VEC + VEC_BYTES;       // key-major: 8 warps x distances
+    static constexpr int OFF_BAR = OFF_HIST + (KV ? 8 * (kMaxDistEntries + 1) * 4 : 0);
+    static constexpr int B_STAT = 0, B_FULL1 = 1, B_EMPTY1 = B_FULL1 + NS1, B_FULL2 = B_EMPTY1 + NS1,
+                         B_EMPTY2 = B_FULL2 + NS2, B_X1 = B_EMPTY2 + NS2, B_X2 = B_X1 + 1, B_X1FREE = B_X2 + 1,
+                         B_P = B_X1FREE + 1, B_DS = B_P + 1, B_ACC = B_DS + 1,
+                         B_DRAIN = B_ACC + 1, NBARS = B_DRAIN + 1;
+    static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NBARS;
+    static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
+    static constexpr int OFF_RANGE = OFF_ABORT + 4;            // first and last visible distance
+    static constexpr int SMEM_USED = OFF_RANGE + 8;
+    // + slack for 1024-byte alignment; at least 116 KB so that one CTA (and its 512 TMEM
+    // columns) owns an SM even for small d
+    static constexpr int SMEM_BYTES = SMEM_USED + 1024 > 118784 ? SMEM_USED + 1024 : 118784;
+    static_assert(SMEM_BYTES <= kMaxSmem, "shared memory overflow");
+    // TMEM: X1 = S (or S^T), X2 = dP (or dP^T); P^T (key-major) and dS (both kernels) are written
+    // in bf16 over the first half of each warpgroup's 64 columns of X1 and X2
+    static constexpr uint32_t COL_X1 = 0, COL_X2 = 128, COL_ACC1 = 256, COL_ACC2 = 256 + D, NCOLS = 512;
+    static_assert(COL_ACC2 + D <= NCOLS, "TMEM overflow");
+};
+
+// TMEM column of K-step kk (16 streamed rows) of a bf16 operand written by the two softmax
+// warpgroups over their own halves of a 128-column score region: rows 0..63 -> columns 0..31,
+// rows 64..127 -> columns 64..95.
+__device__ __forceinline__ uint32_t half_packed_col(int kk) { return kk < 4 ? 8 * kk : 64 + 8 * (kk - 4); }
+
+// 4-byte cp.async of one fp32 per tile row (L or D of the row's token and head); tr holds the
+// token rows of this lane's two tile rows 64*pw + lane and 64*pw + 32 + lane.
+__device__ __forceinline__ void load_vec(uint32_t dst, const float* __restrict__ src, const TileRows& tr,
+                                         int pw, int lane) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = 64 * pw + 32 * half + lane;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4u * r),
+                     "l"(src + (half ? tr.rb : tr.ra))
+                     : "memory");
+    }
+}
+
+template <int D, bool KV>
+__global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(const FramesBwdParams p) {
+    using C = BwdCfg<D, KV>;
+    // the tiles that see most come first under a causal map: early keys, late queries
+    const int tile = KV ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
+    const int head = blockIdx.y;
+    const int seq = blockIdx.z;
+    const int q2 = p.g.Ph * p.g.Pw;
+    const int b = seq / q2, c = seq % q2, ci = c / p.g.Pw, cj = c % p.g.Pw;
+    const int Rc = p.g.Rc[ci], Sc = p.g.Sc[cj], nF = Rc * Sc;
+    const int n_c = p.g.T * nF;
+    const int first = tile * kTileRows;
+    if (first >= n_c) return;  // uniform over the CTA, before any shared state
+    RowMap rows;
+    rows.init(p.g.T, p.g.H, p.g.W, p.g.heads, p.g.Ph, p.g.Pw, p.g.mode, ci, cj, Rc, Sc, b, head);
+    FastDiv dF;
+    dF.init(nF);
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw_base + pad;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM_SLOT);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+    int* range = reinterpret_cast<int*>(smem + C::OFF_RANGE);
+    const float* vecs = reinterpret_cast<const float*>(smem + C::OFF_VEC);
+    float* hist = reinterpret_cast<float*>(smem + C::OFF_HIST);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint64_t lim = p.wait_limit_ns;
+    const int dmax = p.bias.D;
+    const float* bias2 = p.bias2 + static_cast<size_t>(head) * (2 * dmax + 1) + dmax;  // by distance
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar(C::B_STAT), kBwdProducers);
+        for (int s = 0; s < C::NS1; ++s) {
+            ptx::mbar_init(bar(C::B_FULL1 + s), kBwdProducers / 2);  // one producer pair per tensor
+            ptx::mbar_init(bar(C::B_EMPTY1 + s), 1);
+        }
+        for (int s = 0; s < C::NS2; ++s) {
+            ptx::mbar_init(bar(C::B_FULL2 + s), kBwdProducers / 2);
+            ptx::mbar_init(bar(C::B_EMPTY2 + s), 1);
+        }
+        ptx::mbar_init(bar(C::B_X1), 1);
+        ptx::mbar_init(bar(C::B_X2), 1);
+        ptx::mbar_init(bar(C::B_X1FREE), kBwdSoftmax);
+        ptx::mbar_init(bar(C::B_P), kBwdSoftmax);
+        ptx::mbar_init(bar(C::B_DS), kBwdSoftmax);
+        ptx::mbar_init(bar(C::B_ACC), 1);
+        ptx::mbar_init(bar(C::B_DRAIN), 1);
+        *abort = 0;
+        range[0] = dmax + 1;
+        range[1] = -dmax - 1;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kBwdMma) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::NCOLS);
+        ptx::tmem_relinquish();
+    }
+    if (KV)
+        for (int i = threadIdx.x; i < 8 * p.ND; i += kBwdThreads) hist[i] = 0.f;
+    int dlo = dmax + 1, dhi = -dmax - 1;  // first and last visible distance
+    for (int u = static_cast<int>(threadIdx.x) - dmax; u <= dmax; u += kBwdThreads)
+        if (__ldg(bias2 + u) != -INFINITY) {
+            dlo = min(dlo, u);
+            dhi = max(dhi, u);
+        }
+    dlo = __reduce_min_sync(0xffffffffu, dlo);
+    dhi = __reduce_max_sync(0xffffffffu, dhi);
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (lane == 0 && dlo <= dhi) {
+        atomicMin(&range[0], dlo);
+        atomicMax(&range[1], dhi);
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    dlo = range[0];
+    dhi = range[1];
+    // streamed frames that some stationary row sees (the end distances stand for all beyond them)
+    int f_lo = 0, f_hi = p.g.T - 1;
+    {
+        const int ta = dF.div(first), tb = dF.div(min(first + kTileRows, n_c) - 1);
+        if (KV) {  // query frame - key frame in [dlo, dhi]
+            if (dlo > -dmax) f_lo = max(f_lo, ta + dlo);
+            if (dhi < dmax) f_hi = min(f_hi, tb + dhi);
+        } else {
+            if (dhi < dmax) f_lo = max(f_lo, ta - dhi);
+            if (dlo > -dmax) f_hi = min(f_hi, tb - dlo);
+        }
+        if (dlo > dhi) f_hi = f_lo - 1;
+    }
+    const int jbeg = f_lo * nF, jend = (f_hi + 1) * nF;
+    const int nstream = f_hi >= f_lo ? (jend - jbeg + kTileRows - 1) / kTileRows : 0;
+
+    // stationary tiles: (K, V) for the key-major kernel, (Q, dO) for the query-major one
+    const uint16_t* g_a1 = KV ? p.k : p.q;
+    const uint16_t* g_a2 = KV ? p.v : p.dout;
+    const uint16_t* g_b1 = KV ? p.q : p.k;
+    const uint16_t* g_b2 = KV ? p.dout : p.v;
+
+    if (warp >= kBwdProd0 && warp < kBwdProd0 + 4) {
+        // ------------------------------------------------------------------ producers
+        // Pair 0 (warps 8-9) copies the first streamed tensor (and the L/D statistics), pair 1
+        // (warps 10-11) the second; within a pair, warp pw copies rows [64pw, 64pw+64).
+        const int pair = (warp - kBwdProd0) >> 1;
+        const int pw = (warp - kBwdProd0) & 1;
+        const int ns = pair ? C::NS2 : C::NS1;
+        if (nstream > 0) {
+            const TileRows ta = tile_rows(rows, first, n_c, pw, lane, p.nrows, p.status);
+            load_tile_rows<D>(sbase + (pair ? C::OFF_A2 : C::OFF_A1), pair ? g_a2 : g_a1, ta, pw, lane);
+            if (!KV && pair == 0) {  // the stationary queries' L and D
+                load_vec(sbase + C::OFF_VEC, p.lse2, ta, pw, lane);
+                load_vec(sbase + C::OFF_VEC + 4 * kTileRows, p.delta, ta, pw, lane);
+            }
+            cp_async_arrive_noinc(bar(C::B_STAT));
+        }
+        bool ok = true;
+        for (int j = 0; j < nstream; ++j) {
+            const int s = j % ns;
+            if (j >= ns) {
+                int w_ok = 1;
+                if (lane == 0)
+                    w_ok = ptx::mbar_wait(bar((pair ? C::B_EMPTY2 : C::B_EMPTY1) + s), ((j / ns) - 1) & 1, abort, lim);
+                w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
+                if (!w_ok) {
+                    ok = false;
+                    break;
+                }
+            }
+            const TileRows tr = tile_rows(rows, jbeg + j * kTileRows, jend, pw, lane, p.nrows, p.status);
+            load_tile_rows<D>(sbase + (pair ? C::OFF_B2 : C::OFF_B1) + s * C::TILE_BYTES, pair ? g_b2 : g_b1, tr,
+                              pw, lane);
+            if (KV && pair == 0) {  // the streamed queries' L and D
+                const uint32_t v = sbase + C::OFF_VEC + s * 2 * 4 * kTileRows;
+                load_vec(v, p.lse2, tr, pw, lane);
+                load_vec(v + 4 * kTileRows, p.delta, tr, pw, lane);
+            }
+            // completes when this tile has landed; test hook: one thread of the key-major kernel
+            // never signals the first streamed tile
+            if (!(KV && p.fault == 1 && j == 0 && pair == 0 && pw == 0 && lane == 0))
+                cp_async_arrive_noinc(bar((pair ? C::B_FULL2 : C::B_FULL1) + s));
+        }
+        cp_async_commit();
+        cp_async_wait<0>();  // no copy of this thread outlives it
+        if (!ok) record_abort(abort, p.status);
+    } else if (warp == kBwdMma) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0 && nstream > 0) {
+            const uint32_t idesc_x = ptx::idesc_bf16_f32(kTileRows, kTileRows, false);
+            const uint32_t idesc_acc = ptx::idesc_bf16_f32(kTileRows, D, true);
+            const uint64_t a1 = ptx::smem_desc(sbase + C::OFF_A1, 16, 8 * C::SW, C::LAYOUT);
+            const uint64_t a2 = ptx::smem_desc(sbase + C::OFF_A2, 16, 8 * C::SW, C::LAYOUT);
+            // streamed tiles read K-major (as the B of S, dP) or MN-major (as the B of dV, dK, dQ)
+            auto bk = [&](int off) { return ptx::smem_desc(sbase + off, 16, 8 * C::SW, C::LAYOUT); };
+            auto bm = [&](int off) { return ptx::smem_desc(sbase + off, C::BOX_BYTES, 8 * C::SW, C::LAYOUT); };
+            auto x_mma = [&](uint64_t a, uint64_t b, uint32_t d_tmem) {   // D = A B^T over d
+#pragma unroll
+                for (int kk = 0; kk < C::KSTEPS; ++kk) {
+                    const uint32_t off = C::kstep_off(kk) >> 4;
+                    ptx::mma_ss(d_tmem, a + off, b + off, idesc_x, kk > 0 ? 1u : 0u);
+                }
+            };
+            // D += A B over the 128 streamed rows, A from TMEM (P^T, dS^T or dS, half-packed columns)
+            auto acc_mma = [&](uint32_t a_col, uint64_t b, uint32_t d_tmem, bool acc) {
+#pragma unroll
+                for (int kk = 0; kk < kTileRows / 16; ++kk)
+                    ptx::mma_ts(d_tmem, tmem + a_col + half_packed_col(kk), b + ((kk * 16 * C::SW) >> 4),
+                                idesc_acc, (acc || kk > 0) ? 1u : 0u);
+            };
+            auto b1_off = [&](int j) { return C::OFF_B1 + (j % C::NS1) * C::TILE_BYTES; };
+            auto b2_off = [&](int j) { return C::OFF_B2 + (j % C::NS2) * C::TILE_BYTES; };
+            // S (or S^T) of streamed tile j into X1; dP (or dP^T) into X2
+            auto issue_x1 = [&](int j) {
+                fence_proxy_async();  // the cp.async data, observed through the barrier, for the MMA
+                ptx::tc_fence_after();
+                x_mma(a1, bk(b1_off(j)), tmem + C::COL_X1);
+                ptx::mma_commit(bar(C::B_X1));
+            };
+            auto issue_x2 = [&](int j) {
+                fence_proxy_async();
+                ptx::tc_fence_after();
+                x_mma(a2, bk(b2_off(j)), tmem + C::COL_X2);
+                ptx::mma_commit(bar(C::B_X2));
+                if (!KV) ptx::mma_commit(bar(C::B_EMPTY2 + j % C::NS2));  // V_j: dP was its last reader
+            };
+            bool ok = ptx::mbar_wait(bar(C::B_STAT), 0, abort, lim);
+            if (ok) fence_proxy_async();
+            ok = ok && ptx::mbar_wait(bar(C::B_FULL1), 0, abort, lim);
+            if (ok) issue_x1(0);
+            ok = ok && ptx::mbar_wait(bar(C::B_FULL2), 0, abort, lim);
+            if (ok) issue_x2(0);
+            auto wait = [&](int b, int parity) { return ptx::mbar_wait(bar(b), parity, abort, lim); };
+            // Per streamed tile j, in a fixed order (each wait suspends the thread in hardware until
+            // its phase completes):
+            //   key-major  : dV(j) once P^T(j) is in TMEM, S^T(j+1) (over the columns dV(j) has just
+            //                read), dK(j) once dS^T(j) is in TMEM, dP^T(j+1) (over dS^T(j)'s columns)
+            //   query-major: S(j+1) once the softmax has read S(j), dQ(j) once dS(j) is in TMEM,
+            //                dP(j+1) (over dS(j)'s columns)
+            for (int j = 0; ok && j < nstream; ++j) {
+                const bool more = j + 1 < nstream;
+                if (KV) {
+                    ok = wait(C::B_P, j & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    acc_mma(C::COL_X1, bm(b2_off(j)), tmem + C::COL_ACC1, j > 0);  // dV += P^T dO
+                    ptx::mma_commit(bar(C::B_EMPTY2 + j % C::NS2));                 // dO_j: dV was its last reader
+                } else {
+                    ok = wait(C::B_X1FREE, j & 1);
+                    if (!ok) break;
+                }
+                if (more) {
+                    ok = wait(C::B_FULL1 + (j + 1) % C::NS1, ((j + 1) / C::NS1) & 1);
+                    if (!ok) break;
+                    issue_x1(j + 1);
+                }
+                ok = wait(C::B_DS, j & 1);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                // key-major: dK += dS^T Q ; query-major: dQ += dS K
+                acc_mma(C::COL_X2, bm(b1_off(j)), tmem + (KV ? C::COL_ACC2 : C::COL_ACC1), j > 0);
+                ptx::mma_commit(bar(C::B_EMPTY1 + j % C::NS1));  // B1 of tile j: its last reader
+                if (more) {
+                    ok = wait(C::B_FULL2 + (j + 1) % C::NS2, ((j + 1) / C::NS2) & 1);
+                    if (!ok) break;
+                    issue_x2(j + 1);
+                }
+            }
+            if (ok) {
+                ptx::mma_commit(bar(C::B_ACC));
+            } else {
+                record_abort(abort, p.status);
+            }
+            // every MMA issued by this thread must finish before TMEM is released
+            ptx::mma_commit(bar(C::B_DRAIN));
+            volatile int never = 0;
+            ptx::mbar_wait(bar(C::B_DRAIN), 0, &never, lim);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ softmax halves
+        const int h = warp >> 2;                        // streamed columns [64h, 64h+64)
+        const int row = threadIdx.x & 127;              // TMEM lane == stationary row
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t x1 = tmem + lane_base + C::COL_X1 + 64 * h;
+        const uint32_t x2 = tmem + lane_base + C::COL_X2 + 64 * h;
+        const float sl2 = p.scale_log2;
+        const bool row_real = first + row < n_c;
+        const int t_row = dF.div(min(first + row, n_c - 1));
+        // bias of this row and streamed frame f
+        auto bias_of = [&](int f) { return __ldg(bias2 + clamp_dist(KV ? f - t_row : t_row - f, dmax)); };
+        // Key-major: adds v, this row's sum of dS over queries of frame f, to the warp's table of
+        // distances. Rows of equal distance are neighbours: their sum forms in the first of them.
+        float* my_hist = hist + warp * p.ND;
+        auto add_hist = [&](float v, int f) {
+            const int u = clamp_dist(f - t_row, p.Dn) + p.Dn;
+            if (!row_real) v = 0.f;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float other = __shfl_down_sync(0xffffffffu, v, o);
+                const int uo = __shfl_down_sync(0xffffffffu, u, o);
+                if (lane + o < 32 && uo == u) v += other;
+            }
+            const int before = __shfl_up_sync(0xffffffffu, u, 1);
+            if (lane == 0 || before != u) my_hist[u] += v;
+            __syncwarp();  // the next addition may come from another lane
+        };
+        float acc = 0.f;   // sum of dS over the queries of frame f_acc so far
+        int f_acc = -1;
+        float row_l2 = 0.f, row_d = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nstream; ++j) {
+            const int s1 = j % C::NS1;
+            const int j0 = jbeg + j * kTileRows + 64 * h;
+            const int valid = jend - j0;               // streamed rows in this half (may be <= 0)
+            const int f0 = dF.div(j0);
+            const int border = (f0 + 1) * nF - j0;     // column where the next frame starts
+            float off = bias_of(f0);
+            // every wait of a softmax warp is made uniform over the warp: the tcgen05.ld/st below
+            // are .sync.aligned and need all 32 lanes
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_X1), j & 1, abort, lim))) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            // the L/D vectors were written by the producers' cp.async: observe their barrier too
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(KV ? bar(C::B_FULL1 + s1) : bar(C::B_STAT),
+                                                        KV ? (j / C::NS1) & 1 : 0, abort, lim))) {
+                ok = false;
+                break;
+            }
+            if (!KV && j == 0) {
+                row_l2 = vecs[row];
+                row_d = vecs[kTileRows + row];
+            }
+            const float* col_l = vecs + s1 * 2 * kTileRows + 64 * h;   // key-major: per column
+            const float* col_d = col_l + kTileRows;
+            float pr[64];
+            {
+                uint32_t xv[64];
+                ptx::tmem_ld32(x1, *reinterpret_cast<uint32_t(*)[32]>(&xv[0]));
+                ptx::tmem_ld32(x1 + 32, *reinterpret_cast<uint32_t(*)[32]>(&xv[32]));
+                ptx::tmem_wait_ld();
+                if (!KV) {  // S is in registers: the tensor core may compute the next tile's S
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(bar(C::B_X1FREE));
+                }
+                if (border >= 64) {
+#pragma unroll
+                    for (int e4 = 0; e4 < 16; ++e4) {
+                        float4 l4 = make_float4(row_l2, row_l2, row_l2, row_l2);
+                        if (KV) l4 = reinterpret_cast<const float4*>(col_l)[e4];
+                        pr[4 * e4] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4]), sl2, off - l4.x));
+                        pr[4 * e4 + 1] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4 + 1]), sl2, off - l4.y));
+                        pr[4 * e4 + 2] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4 + 2]), sl2, off - l4.z));
+                        pr[4 * e4 + 3] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4 + 3]), sl2, off - l4.w));
+                    }
+                } else {  // a frame starts inside these columns
+                    int f = f0, next = border;
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        if (e == next) {
+                            next += nF;
+                            off = bias_of(++f);
+                        }
+                        pr[e] = ptx::ex2_approx(fmaf(__uint_as_float(xv[e]), sl2, off - (KV ? col_l[e] : row_l2)));
+                    }
+                }
+                if (valid < 64) {  // the ragged last tile: repeated streamed rows give 0
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (e >= valid) pr[e] = 0.f;
+                }
+            }
+            if (KV) {  // P^T for dV += P^T dO
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = ptx::pack_bf16x2(pr[32 * g + 2 * e], pr[32 * g + 2 * e + 1]);
+                    ptx::tmem_st16(x1 + 16 * g, pk);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(C::B_P));
+                if (f_acc != f0) {  // uniform over the warp: all rows see the same columns
+                    if (f_acc >= 0) add_hist(acc, f_acc);
+                    acc = 0.f;
+                    f_acc = f0;
+                }
+            }
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_X2), j & 1, abort, lim))) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            int next = border;  // key-major: column, from the chunk's first, where the frame changes next
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                // 32 columns at a time: 13 warps leave 128 registers a thread, and P is live
+                uint32_t dv[32];
+                ptx::tmem_ld32(x2 + 32 * g, dv);
+                ptx::tmem_wait_ld();
+                uint32_t pk[16];
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e4 = 0; e4 < 4; ++e4) {
+                    const int e0 = 32 * g + 8 * e4;
+                    float dcol[8];
+                    if (KV) {  // key-major: each column's D, four at a time
+                        const float4 a = reinterpret_cast<const float4*>(col_d)[e0 / 4];
+                        const float4 b = reinterpret_cast<const float4*>(col_d)[e0 / 4 + 1];
+                        dcol[0] = a.x; dcol[1] = a.y; dcol[2] = a.z; dcol[3] = a.w;
+                        dcol[4] = b.x; dcol[5] = b.y; dcol[6] = b.z; dcol[7] = b.w;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dcol[e] = row_d;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 8 * e4 + 2 * e;  // column inside this 32-column chunk
+                        // two columns per instruction (packed f32x2): dP - D (exact, as an FMA with
+                        // -1), then P * (dP - D)
+                        const float2 x = __ffma2_rn(make_float2(dcol[2 * e], dcol[2 * e + 1]), make_float2(-1.f, -1.f),
+                                                    make_float2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])));
+                        const float2 sv = __fmul2_rn(make_float2(pr[32 * g + c], pr[32 * g + c + 1]), x);
+                        pk[4 * e4 + e] = ptx::pack_bf16x2(sv.x, sv.y);
+                        if (KV) {
+                            sum = __fadd2_rn(sum, sv);
+                            dv[c] = __float_as_uint(sv.x);
+                            dv[c + 1] = __float_as_uint(sv.y);
+                        }
+                    }
+                }
+                ptx::tmem_st16(x2 + 16 * g, pk);
+                if (KV) {
+                    if (next >= 32) {
+                        acc += sum.x + sum.y;
+                    } else {  // frames end in this chunk: sum each one's columns
+                        int lo = 0;
+#pragma unroll 1
+                        while (lo < 32) {
+                            const int hi = min(next, 32);
+                            float s = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s += (e >= lo && e < hi) ? __uint_as_float(dv[e]) : 0.f;
+                            acc += s;
+                            if (hi < 32) {
+                                add_hist(acc, f_acc);
+                                acc = 0.f;
+                                ++f_acc;
+                                next += nF;
+                            }
+                            lo = hi;
+                        }
+                    }
+                    next -= 32;
+                }
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(C::B_DS));
+            // a frame that ends with these columns is added when the next tile's frame differs;
+            // f_acc is the frame of the last column
+        }
+        if (KV && ok && f_acc >= 0) add_hist(acc, f_acc);
+        if (ok && (nstream == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_ACC), 0, abort, lim)))) {
+            ptx::tc_fence_after();
+            const int si = first + row;                 // stationary row (key or query)
+            const bool store = si < n_c && row_ok(rows(si), p.nrows, p.status);
+            const size_t grow = store ? static_cast<size_t>(rows(si)) : 0;
+            constexpr int HALF = D / 2;                 // accumulator columns of this warpgroup
+            // key-major: acc1 = dV (unscaled), acc2 = dK ; query-major: acc1 = dQ
+#pragma unroll
+            for (int which = 0; which < (KV ? 2 : 1); ++which) {
+                const uint32_t col = tmem + lane_base + (which ? C::COL_ACC2 : C::COL_ACC1) + HALF * h;
+                const float mul = (KV && which == 0) ? 1.f : p.scale;
+                uint16_t* out = KV ? (which ? p.dk : p.dv) : p.dq;
+#pragma unroll
+                for (int g = 0; g < HALF / 16; ++g) {
+                    uint32_t av[16];
+                    if (nstream > 0) {
+                        ptx::tmem_ld16(col + 16 * g, av);
+                        ptx::tmem_wait_ld();
+                    } else {  // nothing sees this tile
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) av[e] = 0u;
+                    }
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        pk[e] = ptx::pack_bf16x2(__uint_as_float(av[2 * e]) * mul, __uint_as_float(av[2 * e + 1]) * mul);
+                    if (store) {
+                        uint4* dst = reinterpret_cast<uint4*>(out + grow * D + HALF * h + 16 * g);
+                        dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    }
+                }
+            }
+        } else if (!*abort) {
+            record_abort(abort, p.status);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kBwdMma) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::NCOLS);
+    }
+    if (KV) {  // this CTA's sums by distance, its warps' tables added in order
+        float* part = p.part + ((static_cast<size_t>(head) * p.seqs + seq) * p.tiles + tile) * p.ND;
+        for (int u = threadIdx.x; u < p.ND; u += kBwdThreads) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) s += hist[w * p.ND + u];
+            part[u] = s;
+        }
+    }
+}
+
+// D[row] = sum_e dO[row][e] * (O[row][e] + O_lo[row][e]) (16 lanes per 256-byte row, fewer for smaller d), the row's
+// log-sum-exp in log2, and the bias by head and distance in log2.
+template <int D>
+__global__ void __launch_bounds__(256) skiparse_frames_stats_kernel(const FramesBwdParams p, long long nrows) {
+    constexpr int LPR = D / 8;            // lanes per row (8 bf16 = 16 bytes per lane)
+    constexpr int RPW = 32 / LPR;         // rows per warp step
+    const int lane = threadIdx.x & 31;
+    const long long thread = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long r0 = (thread >> 5) * RPW; r0 < nrows; r0 += (nthreads >> 5) * RPW) {
+        const long long r = r0 + lane / LPR;
+        float acc = 0.f;
+        if (r < nrows) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p.out + r * D + (lane % LPR) * 8);
+            const uint4 g = *reinterpret_cast<const uint4*>(p.dout + r * D + (lane % LPR) * 8);
+            uint4 lo = make_uint4(0u, 0u, 0u, 0u);
+            if (p.out_lo) lo = *reinterpret_cast<const uint4*>(p.out_lo + r * D + (lane % LPR) * 8);
+            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w}, lv[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc = fmaf(__uint_as_float(av[e] << 16) + __uint_as_float(lv[e] << 16), __uint_as_float(gv[e] << 16), acc);
+                acc = fmaf(__uint_as_float(av[e] & 0xffff0000u) + __uint_as_float(lv[e] & 0xffff0000u),
+                           __uint_as_float(gv[e] & 0xffff0000u), acc);
+            }
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        if (r < nrows && lane % LPR == 0) {
+            p.delta[r] = acc;
+            const float l = p.lse[r] * kLog2E;
+            p.lse2[r] = l < kLse2Low ? kLse2Low : l;
+        }
+    }
+    const int entries = 2 * p.bias.D + 1;
+    for (long long i = thread; i < static_cast<long long>(p.g.heads) * entries; i += nthreads)
+        p.bias2[i] = bias_log2(p.bias, p.g.heads, static_cast<int>(i % entries), static_cast<int>(i / entries));
+}
+
+// dtable of one head: the workspace's rows added per distance (one warp each), then the distances of
+// each bucket.
+__global__ void __launch_bounds__(512) skiparse_frames_dtable_kernel(const FramesBwdParams p) {
+    __shared__ float sums[kMaxDistEntries];
+    const int head = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q2 = p.g.Ph * p.g.Pw;
+    const float* part = p.part + static_cast<size_t>(head) * p.seqs * p.tiles * p.ND;
+    for (int u = warp; u < p.ND; u += 16) {
+        float s = 0.f;
+        for (int seq = 0; seq < p.seqs; ++seq) {
+            const int c = seq % q2;
+            const int n_c = p.g.T * p.g.Rc[c / p.g.Pw] * p.g.Sc[c % p.g.Pw];
+            const int tiles = (n_c + kTileRows - 1) / kTileRows;  // the others were not launched
+            for (int t = lane; t < tiles; t += 32) s += part[(static_cast<size_t>(seq) * p.tiles + t) * p.ND + u];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) sums[u] = s;
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.bias.NB; g += 512) {
+        float s = 0.f;
+        for (int u = 0; u < p.ND; ++u)
+            if (p.bias.buckets[u - p.Dn + p.bias.D] == g) s += sums[u];
+        p.dtable[static_cast<size_t>(g) * p.g.heads + head] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+    }
+}
+
+template <int D, bool KV>
+int launch_bwd_d(const FramesBwdParams& p, const Geometry& g, cudaStream_t stream) {
+    using C = BwdCfg<D, KV>;
+    // per device: the kernel's shared-memory attribute is set (host threads may race here;
+    // setting it twice is harmless, the flag only has to be a race-free read)
+    static std::atomic<int> attr_done_dev[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (dev < 0 || dev >= 64 || !attr_done_dev[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(skiparse_frames_bwd_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::SMEM_BYTES);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
+    }
+    const dim3 grid(p.tiles, g.heads, p.seqs);
+    skiparse_frames_bwd_kernel<D, KV><<<grid, kBwdThreads, C::SMEM_BYTES, stream>>>(p);
+    return static_cast<int>(cudaGetLastError());
+}
+
+template <int D>
+int launch_bwd_all(const FramesBwdParams& p, const Geometry& g, cudaStream_t st) {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long long nrows = static_cast<long long>(g.B) * g.T * g.H * g.W * g.heads;
+    const long long rows_per_block = 8LL * (32 / (D / 8));
+    long long blocks = (nrows + rows_per_block - 1) / rows_per_block;
+    if (blocks > 16LL * sms) blocks = 16LL * sms;
+    skiparse_frames_stats_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p, nrows);
+    int e = static_cast<int>(cudaGetLastError());
+    if (e) return e;
+    e = launch_bwd_d<D, true>(p, g, st);
+    if (e) return e;
+    e = launch_bwd_d<D, false>(p, g, st);
+    if (e) return e;
+    skiparse_frames_dtable_kernel<<<g.heads, 512, 0, st>>>(p);
+    return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_frames_bwd(const FramesBwdParams& p, const Geometry& g, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (g.d) {
+        case 32: return launch_bwd_all<32>(p, g, st);
+        case 64: return launch_bwd_all<64>(p, g, st);
+        case 128: return launch_bwd_all<128>(p, g, st);
+        default: return static_cast<int>(cudaErrorInvalidValue);
+    }
+}
+
+}  // namespace skiparse

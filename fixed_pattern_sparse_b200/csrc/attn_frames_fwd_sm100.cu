@@ -1,0 +1,701 @@
+// attn_frames_fwd_sm100.cu -- class attention with a learned bias by frame distance, forward, over
+// bf16 keys and values or over the e4m3 frame cache (sm_100a).
+//
+// For one (b, class, head) subsequence, a query x at frame t_x and a key y at frame t_y:
+//   s_xy = q_x . k_y / sqrt(d) + bias[clamp(t_x - t_y, -D, D)],   out_x = softmax_y(s_xy) v_y,
+// where a bias of -inf masks the pair; a row without a visible key gives 0 (lse -inf).
+//
+// The schedule is that of the unbiased forward (attn_fwd_sm100.cu): a CTA owns 256 queries as two
+// 128-row tiles, streams 128-key tiles of K and V through shared-memory rings of two slots,
+// S = Q K^T and O += P V run on tcgen05 with S, P and O in TMEM, one thread per query row does
+// the online softmax with the lazy rescale. What the frames add:
+//   * The bias is constant over the tokens of a frame, so a key tile inside one frame (all but
+//     one in Rc*Sc/128 tiles of a large latent) needs one table lookup per row and tile, folded
+//     into the softmax's existing FMA: no instruction per score. A tile that crosses a
+//     frame border adds the bias per 32-key chunk, and in the chunk with the border per key.
+//   * The frames that some row of the CTA can see form a range, from the first and last visible
+//     distance of the table; only its keys are loaded. With a causal map that is half the work.
+//     Query tiles are launched last frame first, so that the longest ones start first.
+//   * Cached keys are e4m3 codes. Three producer warps read them with 16-byte loads one tile
+//     ahead into registers, expand them to bf16 (exactly: the scale is a power of two, see
+//     frames_common.cuh) and store them into the swizzled tile, so the tensor-core side and its
+//     precision are those of bf16 keys at half the cache traffic.
+//   * Few query tiles over a long cache leave SMs idle: the key range is then cut into `splits`
+//     parts, each CTA writes its normalised partial output and log-sum-exp in fp32, and
+//     a second kernel joins them.
+// Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "frames_common.cuh"
+
+namespace skiparse {
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBN = 128;
+constexpr int kProdWarp0 = 8;
+constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by more than 2^8
+constexpr int kPParts = 2;            // P is released to the tensor core in two halves of the key tile
+
+template <int D, bool CACHE>
+struct Cfg : TileGeom<D> {
+    using G = TileGeom<D>;
+    using G::TILE_BYTES;
+    static constexpr int PROD_WARPS = CACHE ? 3 : 2;
+    static constexpr int MMA_WARP = kProdWarp0 + PROD_WARPS;
+    static constexpr int THREADS = 32 * (MMA_WARP + 1);
+    static constexpr int FULL_COUNT = CACHE ? PROD_WARPS : 32 * PROD_WARPS;  // arrivals per tile
+    static constexpr int KST = 2, VST = 2;
+    static constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_O0 = 256, COL_O1 = 256 + D;
+    static constexpr uint32_t NCOLS = 512;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = 2 * TILE_BYTES;
+    static constexpr int OFF_V = OFF_K + KST * TILE_BYTES;
+    static constexpr int OFF_TAB = OFF_V + VST * TILE_BYTES;  // bias by distance index
+    static constexpr int OFF_BAR = OFF_TAB + 4 * (kMaxDistEntries + 1);
+    static constexpr int B_Q = 0;
+    static constexpr int B_KFULL = 1;
+    static constexpr int B_KEMPTY = B_KFULL + KST;
+    static constexpr int B_VFULL = B_KEMPTY + KST;
+    static constexpr int B_VEMPTY = B_VFULL + VST;
+    static constexpr int B_SFULL = B_VEMPTY + VST;
+    static constexpr int B_PFULL = B_SFULL + 2;
+    static constexpr int B_OFULL = B_PFULL + 2 * kPParts;
+    static constexpr int B_DRAIN = B_OFULL + 1;
+    static constexpr int NBARS = B_DRAIN + 1;
+    static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NBARS;
+    static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
+    static constexpr int OFF_RANGE = OFF_ABORT + 4;  // first and last visible distance
+    static constexpr int SMEM_USED = OFF_RANGE + 8;
+    // + slack for 1024-byte alignment; at least 116 KB so that one CTA (and its 512 TMEM
+    // columns) owns an SM even for small d
+    static constexpr int SMEM_BYTES = SMEM_USED + 1024 > 118784 ? SMEM_USED + 1024 : 118784;
+    static_assert(COL_O1 + D <= NCOLS, "TMEM overflow");
+    static_assert(SMEM_BYTES <= 232448, "shared memory overflow");
+};
+
+// The rows of a 128-key tile that one producer lane expands: 16 codes (one 16-byte chunk) of
+// every third row group of its warp.
+template <int D>
+struct CacheTile {
+    static constexpr int CPR = D / 16;            // chunks per row of codes
+    static constexpr int RPI = 32 / CPR;          // rows per warp instruction
+    static constexpr int NG = kBN / RPI;          // row groups of a tile
+    static constexpr int PER = (NG + 2) / 3;      // row groups of a warp
+    uint4 x[PER];
+    uint32_t sc[PER];
+
+    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int j0,
+                                         int jend, const FastDiv& dF, int nF, int F, int NBk, int cap, int pw, int lane,
+                                         int* status) {
+        const int c = lane % CPR, rsub = lane / CPR;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int g = pw + 3 * i;
+            if (g < NG) {
+                const int j = min(j0 + g * RPI + rsub, jend - 1);  // rows past the end repeat the last one
+                const int slot = dF.div(j), at = j - slot * nF;
+                const long long row = load_row(static_cast<long long>(slot) * F + at,
+                                               static_cast<long long>(cap) * F, status);
+                x[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * D) + c);
+                sc[i] = __ldg(scales + static_cast<long long>(slot) * NBk + at / kCacheBlock);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t dst, int pw, int lane) const {
+        using C = TileGeom<D>;
+        const int c = lane % CPR, rsub = lane / CPR;
+        const uint32_t box = static_cast<uint32_t>(c * 32) / C::SW;
+        const uint32_t cb = static_cast<uint32_t>(c * 32) % C::SW / 16;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int g = pw + 3 * i;
+            if (g < NG) {
+                const int r = g * RPI + rsub;
+                const uint32_t m = scale_mul(sc[i]);
+                uint32_t y[8];
+                e4m3x4_to_bf16(x[i].x, m, y[0], y[1]);
+                e4m3x4_to_bf16(x[i].y, m, y[2], y[3]);
+                e4m3x4_to_bf16(x[i].z, m, y[4], y[5]);
+                e4m3x4_to_bf16(x[i].w, m, y[6], y[7]);
+                if (__any_sync(0xffffffffu, sc[i] > 134u)) {  // magnitudes beyond 57344
+                    const uint32_t rest = scale_rest(sc[i]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = bf16x2_mul(y[e], rest);
+                }
+                const uint32_t sw = C::SW == 128 ? static_cast<uint32_t>(r & 7) : static_cast<uint32_t>((r >> 1) & 3);
+                const uint32_t base = dst + box * C::BOX_BYTES + static_cast<uint32_t>(r) * C::SW;
+                // two 16-byte stores; the lanes of a row's second box start with their second
+                // half, so that the eight lanes of a row never meet in a bank
+                const bool flip = box & 1u;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t hi = flip ? 1u - half : half;
+                    const uint32_t a = base + (((cb + hi) ^ sw) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(hi ? y[4] : y[0]),
+                                 "r"(hi ? y[5] : y[1]), "r"(hi ? y[6] : y[2]), "r"(hi ? y[7] : y[3])
+                                 : "memory");
+                }
+            }
+        }
+    }
+};
+
+template <int D, bool CACHE>
+__global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frames_kernel(const FramesFwdParams p) {
+    using C = Cfg<D, CACHE>;
+    const int npairs = gridDim.x / p.splits;
+    const int split = blockIdx.x % p.splits;
+    const int pair = npairs - 1 - blockIdx.x / p.splits;
+    const int head = blockIdx.y;
+    const int seq = blockIdx.z;
+    const int q2 = p.g.Ph * p.g.Pw;
+    const int b = seq / q2, c = seq % q2, ci = c / p.g.Pw, cj = c % p.g.Pw;
+    const int Rc = p.g.Rc[ci], Sc = p.g.Sc[cj], nF = Rc * Sc;
+    const int n_q = p.g.T * nF;
+    const int q_first = pair * 2 * kBM;
+    if (q_first >= n_q) return;  // uniform over the CTA, before any shared state
+    int start = 0;
+    if (CACHE) {
+        start = p.cache.start[b];
+        if (start < 0 || start > kMaxStart) return;  // a sequence without new frames
+    }
+    const int end = start + p.g.T;                  // frames up to the newest query's
+    const bool wrapped = CACHE && end > p.cache.cap;  // every slot of the ring is in use
+    const int nframes = wrapped ? p.cache.cap : end;  // frames (slots) that hold keys
+    // frame of slot f: f + fbase, one turn of the ring earlier beyond the newest slot
+    const int fnew = wrapped ? (end - 1) % p.cache.cap : nframes;
+    const int fbase = wrapped ? end - 1 - fnew : 0;
+    auto frame_time = [&](int f) { return f + fbase - (f > fnew ? p.cache.cap : 0); };
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_base = ptx::smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw_base + pad;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM_SLOT);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+    float* tab = reinterpret_cast<float*>(smem + C::OFF_TAB);
+    int* range = reinterpret_cast<int*>(smem + C::OFF_RANGE);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint64_t lim = p.wait_limit_ns;
+    const int dmax = p.bias.D;
+    RowMap rows;
+    rows.init(p.g.T, p.g.H, p.g.W, p.g.heads, p.g.Ph, p.g.Pw, p.g.mode, ci, cj, Rc, Sc, b, head);
+    FastDiv dF;
+    dF.init(nF);
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar(C::B_Q), 64);
+        for (int s = 0; s < C::KST; ++s) {
+            ptx::mbar_init(bar(C::B_KFULL + s), C::FULL_COUNT);
+            ptx::mbar_init(bar(C::B_KEMPTY + s), 1);
+        }
+        for (int s = 0; s < C::VST; ++s) {
+            ptx::mbar_init(bar(C::B_VFULL + s), C::FULL_COUNT);
+            ptx::mbar_init(bar(C::B_VEMPTY + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(C::B_SFULL + i), 1);
+            for (int h = 0; h < kPParts; ++h) ptx::mbar_init(bar(C::B_PFULL + kPParts * i + h), kBM);
+        }
+        ptx::mbar_init(bar(C::B_OFULL), 1);
+        ptx::mbar_init(bar(C::B_DRAIN), 1);
+        *abort = 0;
+        range[0] = dmax + 1;
+        range[1] = -dmax - 1;
+        ptx::fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::NCOLS);
+        ptx::tmem_relinquish();
+    }
+    // the bias by distance, and the first and last distance that is visible
+    int dlo = dmax + 1, dhi = -dmax - 1;
+    for (int u = threadIdx.x; u <= 2 * dmax; u += C::THREADS) {
+        const float v = bias_log2(p.bias, p.g.heads, u, head);
+        tab[u] = v;
+        if (v != -INFINITY) {
+            dlo = min(dlo, u - dmax);
+            dhi = max(dhi, u - dmax);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    dlo = __reduce_min_sync(0xffffffffu, dlo);
+    dhi = __reduce_max_sync(0xffffffffu, dhi);
+    if (lane == 0 && dlo <= dhi) {
+        atomicMin(&range[0], dlo);
+        atomicMax(&range[1], dhi);
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    dlo = range[0];
+    dhi = range[1];
+    // frames that some row of this CTA can see (the end distances stand for all beyond them); a
+    // wrapped ring keeps its frames out of order, and all of its slots are read
+    int f_lo = 0, f_hi = nframes - 1;
+    if (!wrapped) {
+        const int ta = start + dF.div(q_first), tb = start + dF.div(min(q_first + 2 * kBM, n_q) - 1);
+        if (dhi < dmax) f_lo = max(f_lo, ta - dhi);
+        if (dlo > -dmax) f_hi = min(f_hi, tb - dlo);
+    }
+    if (dlo > dhi) f_hi = f_lo - 1;
+    const int nkv_all = f_hi >= f_lo ? ((f_hi - f_lo + 1) * nF + kBN - 1) / kBN : 0;
+    const int per_split = (nkv_all + p.splits - 1) / p.splits;
+    const int jend = (f_hi + 1) * nF;                          // end of the visible keys
+    const int jbeg = f_lo * nF + split * per_split * kBN;      // this CTA's first key
+    const int nkv = max(0, min(per_split, nkv_all - split * per_split));
+
+    if (warp >= kProdWarp0) {
+        if (warp < C::MMA_WARP) {
+            // ------------------------------------------------------------------ producers
+            const int pw = warp - kProdWarp0;
+            const int fault_skip = (p.fault == 1 && pw == 0 && lane == 0);
+            bool ok = true;
+            auto wait_empty = [&](bool is_v, int j) {  // the slot of key step j is free
+                const int nst = is_v ? C::VST : C::KST;
+                if (j < nst) return true;
+                int w_ok = 1;
+                if (lane == 0)
+                    w_ok = ptx::mbar_wait(bar((is_v ? C::B_VEMPTY : C::B_KEMPTY) + j % nst), ((j / nst) - 1) & 1, abort, lim);
+                return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+            };
+            if (nkv > 0 && pw < 2) {
+                load_tile<D>(sbase + C::OFF_Q, p.q, rows, q_first, n_q, pw, lane, p.nrows, p.status);
+                load_tile<D>(sbase + C::OFF_Q + C::TILE_BYTES, p.q, rows, q_first + kBM, n_q, pw, lane, p.nrows, p.status);
+                cp_async_arrive_noinc(bar(C::B_Q));
+            }
+            if constexpr (CACHE) {
+                const long long sh = static_cast<long long>(seq) * p.g.heads + head;
+                const long long code0 = sh * p.cache.cap * p.cache.F * D, scale0 = sh * p.cache.cap * p.cache.NBk;
+                CacheTile<D> kt, vt;
+                auto load = [&](CacheTile<D>& t, const uint8_t* codes, const uint8_t* scales, int j) {
+                    t.load(codes + code0, scales + scale0, jbeg + j * kBN, jend, dF, nF, p.cache.F, p.cache.NBk, p.cache.cap,
+                           pw, lane, p.status);
+                };
+                auto release = [&](int full, bool signal) {  // the stores of this warp, for the tensor core
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && signal) ptx::mbar_arrive(bar(full));
+                };
+                if (nkv > 0) load(kt, p.cache.k, p.cache.ks, 0);
+                for (int j = 0; j < nkv; ++j) {
+                    load(vt, p.cache.v, p.cache.vs, j);
+                    if (!(ok = wait_empty(false, j))) break;
+                    kt.store(sbase + C::OFF_K + (j % C::KST) * C::TILE_BYTES, pw, lane);
+                    release(C::B_KFULL + j % C::KST, !(fault_skip && j == 0));  // test hook: one warp never signals
+                    if (j + 1 < nkv) load(kt, p.cache.k, p.cache.ks, j + 1);
+                    if (!(ok = wait_empty(true, j))) break;
+                    vt.store(sbase + C::OFF_V + (j % C::VST) * C::TILE_BYTES, pw, lane);
+                    release(C::B_VFULL + j % C::VST, true);
+                }
+            } else {
+                TileRows kv{0, 0};  // token rows of key step j, shared by its K and V tiles
+                for (int L = 0; L < 2 * nkv; ++L) {
+                    const int j = L >> 1;
+                    const bool is_v = L & 1;
+                    if (!is_v) kv = tile_rows(rows, jbeg + j * kBN, jend, pw, lane, p.nrows, p.status);
+                    if (!(ok = wait_empty(is_v, j))) break;
+                    const int s = j % (is_v ? C::VST : C::KST);
+                    load_tile_rows<D>(sbase + (is_v ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES, is_v ? p.v : p.k, kv, pw, lane);
+                    // test hook: one thread never signals the first K tile
+                    if (!(fault_skip && L == 0)) cp_async_arrive_noinc(bar((is_v ? C::B_VFULL : C::B_KFULL) + s));
+                }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();  // no copy of this thread outlives it
+            if (!ok) record_abort(abort, p.status);
+        } else {
+            // ------------------------------------------------------------------ MMA issuer
+            if (lane == 0 && nkv > 0) {
+                const uint32_t idesc_s = ptx::idesc_bf16_f32(kBM, kBN, false);
+                const uint32_t idesc_o = ptx::idesc_bf16_f32(kBM, D, true);
+                const uint32_t q0 = sbase + C::OFF_Q, q1 = q0 + C::TILE_BYTES;
+                const uint64_t qd0 = ptx::smem_desc(q0, 16, 8 * C::SW, C::LAYOUT);
+                const uint64_t qd1 = ptx::smem_desc(q1, 16, 8 * C::SW, C::LAYOUT);
+                const uint64_t kd0 = ptx::smem_desc(sbase + C::OFF_K, 16, 8 * C::SW, C::LAYOUT);
+                const uint64_t vd0 = ptx::smem_desc(sbase + C::OFF_V, C::BOX_BYTES, 8 * C::SW, C::LAYOUT);
+                auto issue_s = [&](uint64_t qd, int kslot, uint32_t d_tmem) {
+                    const uint64_t kd = kd0 + ((kslot * C::TILE_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < C::KSTEPS; ++kk) {
+                        const uint32_t off = C::kstep_off(kk) >> 4;
+                        ptx::mma_ss(d_tmem, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                };
+                auto issue_o = [&](int qt, int vslot, bool acc, int phase) -> bool {
+                    const uint32_t p_tmem = tmem + (qt ? C::COL_S1 : C::COL_S0);
+                    const uint32_t d_tmem = tmem + (qt ? C::COL_O1 : C::COL_O0);
+                    const uint64_t vd = vd0 + ((vslot * C::TILE_BYTES) >> 4);
+                    constexpr int KPP = kBN / 16 / kPParts;  // K-steps per part
+                    for (int h = 0; h < kPParts; ++h) {
+                        if (!ptx::mbar_wait(bar(C::B_PFULL + kPParts * qt + h), phase, abort, lim)) return false;
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int k4 = 0; k4 < KPP; ++k4) {
+                            const int kk = h * KPP + k4;
+                            ptx::mma_ts(d_tmem, p_tmem + kk * 8, vd + ((kk * 16 * C::SW) >> 4), idesc_o,
+                                        (acc || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    return true;
+                };
+                bool ok = ptx::mbar_wait(bar(C::B_Q), 0, abort, lim) &&
+                          ptx::mbar_wait(bar(C::B_KFULL + 0), 0, abort, lim);
+                if (ok) {
+                    fence_proxy_async();  // cp.async data observed through the barriers, for the MMA
+                    ptx::tc_fence_after();
+                    issue_s(qd0, 0, tmem + C::COL_S0);
+                    ptx::mma_commit(bar(C::B_SFULL + 0));
+                    issue_s(qd1, 0, tmem + C::COL_S1);
+                    ptx::mma_commit(bar(C::B_SFULL + 1));
+                    ptx::mma_commit(bar(C::B_KEMPTY + 0));
+                }
+                for (int j = 0; ok && j < nkv; ++j) {
+                    const int vs = j % C::VST;
+                    const bool v_ok = ptx::mbar_wait(bar(C::B_VFULL + vs), (j / C::VST) & 1, abort, lim);
+                    if (v_ok) fence_proxy_async();
+                    if (!v_ok || !issue_o(0, vs, j > 0, j & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool more = j + 1 < nkv;
+                    const int ks = (j + 1) % C::KST;
+                    if (more) {
+                        if (!ptx::mbar_wait(bar(C::B_KFULL + ks), ((j + 1) / C::KST) & 1, abort, lim)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_proxy_async();
+                        ptx::tc_fence_after();
+                        issue_s(qd0, ks, tmem + C::COL_S0);
+                        ptx::mma_commit(bar(C::B_SFULL + 0));
+                    }
+                    if (!issue_o(1, vs, j > 0, j & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mma_commit(bar(C::B_VEMPTY + vs));
+                    if (more) {
+                        issue_s(qd1, ks, tmem + C::COL_S1);
+                        ptx::mma_commit(bar(C::B_SFULL + 1));
+                        ptx::mma_commit(bar(C::B_KEMPTY + ks));
+                    }
+                }
+                if (ok) {
+                    ptx::mma_commit(bar(C::B_OFULL));
+                } else {
+                    record_abort(abort, p.status);
+                }
+                // every MMA issued by this thread must finish before TMEM is released
+                ptx::mma_commit(bar(C::B_DRAIN));
+                volatile int never = 0;
+                ptx::mbar_wait(bar(C::B_DRAIN), 0, &never, lim);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------------ softmax (WG 0/1)
+        const int qt = warp >> 2;                       // query tile 0 or 1
+        const int row = threadIdx.x & 127;              // TMEM lane == row in the tile
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + (qt ? C::COL_S1 : C::COL_S0);
+        const uint32_t o_col = qt ? C::COL_O1 : C::COL_O0;
+        const uint32_t sfull = bar(C::B_SFULL + qt);
+        const float sl2 = p.scale_log2;
+        const int qi = q_first + qt * kBM + row;
+        const int tq = start + dF.div(min(qi, n_q - 1));
+        auto bias_of = [&](int f) { return tab[clamp_dist(tq - frame_time(f), dmax) + dmax]; };
+        float m_run = -INFINITY, l_run = 0.f;  // in units of log2
+        bool ok = true;
+        for (int j = 0; j < nkv; ++j) {
+            // Every wait of a softmax warp is made uniform over the warp (a lane can see the abort
+            // flag while another sees the phase complete): the tcgen05.ld/st below are
+            // .sync.aligned and need all 32 lanes.
+            const int j0 = jbeg + j * kBN;
+            const int f0 = dF.div(j0);
+            const int border = (f0 + 1) * nF - j0;  // tile column where the next frame starts
+            float off = bias_of(f0), mul = sl2;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(sfull, j & 1, abort, lim))) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            if (border < kBN) {
+                // A frame starts inside the tile: S becomes S * scale + bias in place, 32 columns at
+                // a time, before the softmax below reads the row. `next` is the column (in this
+                // chunk) where the bias changes next.
+                int f = f0, next = border;
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t sv[32];
+                    ptx::tmem_ld32(s_addr + 32 * g, sv);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (e == next) {
+                            ++f;
+                            next += nF;
+                            off = bias_of(f);  // columns past the last frame are masked below
+                        }
+                        sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, off));
+                    }
+                    next -= 32;
+                    ptx::tmem_st16(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+                    ptx::tmem_st16(s_addr + 32 * g + 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+                }
+                ptx::tmem_wait_st();
+                off = 0.f;
+                mul = 1.f;
+            }
+            float sc[kBN];
+            {
+                uint32_t sv[kBN];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    ptx::tmem_ld32(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * g]));
+                ptx::tmem_wait_ld();  // one wait for the whole 128-column row
+#pragma unroll
+                for (int e = 0; e < kBN; ++e) sc[e] = __uint_as_float(sv[e]);
+            }
+            if (j0 + kBN > jend) {
+                const int valid = jend - j0;
+#pragma unroll
+                for (int e = 0; e < kBN; ++e)
+                    if (e >= valid) sc[e] = -INFINITY;
+            }
+            // row max with 3-input max instructions, four independent chains
+            float mx0 = ptx::max3f(sc[0], sc[1], sc[2]), mx1 = ptx::max3f(sc[3], sc[4], sc[5]);
+            float mx2 = ptx::max3f(sc[6], sc[7], sc[8]), mx3 = ptx::max3f(sc[9], sc[10], sc[11]);
+#pragma unroll
+            for (int e = 12; e + 8 <= kBN; e += 8) {
+                mx0 = ptx::max3f(mx0, sc[e], sc[e + 1]);
+                mx1 = ptx::max3f(mx1, sc[e + 2], sc[e + 3]);
+                mx2 = ptx::max3f(mx2, sc[e + 4], sc[e + 5]);
+                mx3 = ptx::max3f(mx3, sc[e + 6], sc[e + 7]);
+            }
+            static_assert((kBN - 12) % 8 == 4, "tail of the max chains");
+            mx0 = ptx::max3f(mx0, sc[kBN - 4], sc[kBN - 3]);
+            mx1 = ptx::max3f(mx1, sc[kBN - 2], sc[kBN - 1]);
+            const float mx = fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), mul, off);
+            float alpha = 1.f;
+            if (j == 0 || mx > m_run + kRescaleLog2) {  // m_run = -inf: O and l are zero, alpha 0 keeps them
+                alpha = (j == 0) ? 0.f : ptx::ex2_approx(m_run - mx);
+                m_run = mx;
+            }
+            // P = 2^(S*scale*log2(e) + bias - m), written as bf16 pairs over the first 64 columns of
+            // S, in two halves released as they are stored. A row that has seen no key yet keeps
+            // the reference 0, so that its -inf scores give 0.
+            const float neg = off - (m_run == -INFINITY ? 0.f : m_run);
+            float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;  // four short addition chains
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float x0 = fmaf(sc[32 * g + 2 * e], mul, neg);
+                    const float x1 = fmaf(sc[32 * g + 2 * e + 1], mul, neg);
+                    const float p0 = ptx::ex2_approx(x0);
+                    const float p1 = ptx::ex2_approx(x1);
+                    if (e & 1) {
+                        sum2 += p0;
+                        sum3 += p1;
+                    } else {
+                        sum0 += p0;
+                        sum1 += p1;
+                    }
+                    pk[e] = ptx::pack_bf16x2(p0, p1);
+                }
+                ptx::tmem_st16(s_addr + 16 * g, pk);
+                if (g == 1 && j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // Rare: a row max grew by more than 2^8. This warp rescales its rows of O_qt
+                    // before releasing the first half of P, i.e. before this tile's P*V
+                    // accumulates into O_qt; O_qt was completed by the previous P*V (the commit
+                    // behind this tile's S covers it).
+#pragma unroll
+                    for (int go = 0; go < D / 16; ++go) {
+                        uint32_t ov[16];
+                        const uint32_t o_addr = tmem + lane_base + o_col + 16 * go;
+                        ptx::tmem_ld16(o_addr, ov);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        ptx::tmem_st16(o_addr, ov);
+                    }
+                }
+                if (g & 1) {
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + (g >> 1)));
+                }
+            }
+            l_run = l_run * alpha + ((sum0 + sum1) + (sum2 + sum3));
+        }
+        if (ok && (nkv == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_OFULL), 0, abort, lim)))) {
+            ptx::tc_fence_after();
+            // a row without a visible key: 0, and -inf for its log-sum-exp
+            const float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;
+            const float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run);
+            const bool real = qi < n_q && row_ok(rows(qi), p.nrows, p.status);
+            const size_t grow = real ? static_cast<size_t>(rows(qi)) : 0;
+            if (real) {
+                if (p.splits > 1)
+                    p.part_l[grow * p.splits + split] = l2;
+                else if (p.lse)
+                    p.lse[grow] = l2 * 0.6931471805599453f;
+            }
+#pragma unroll
+            for (int g = 0; g < D / 32; ++g) {
+                uint32_t ov[32];
+                if (nkv > 0) {
+                    ptx::tmem_ld32(tmem + lane_base + o_col + 32 * g, ov);
+                    ptx::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = 0u;
+                }
+                if (p.splits > 1) {
+                    if (real) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + (grow * p.splits + split) * D + 32 * g);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv_l, __uint_as_float(ov[4 * e + 1]) * inv_l,
+                                                 __uint_as_float(ov[4 * e + 2]) * inv_l, __uint_as_float(ov[4 * e + 3]) * inv_l);
+                    }
+                } else {
+                    auto store = [&](uint16_t* to, const uint32_t(&w)[16]) {
+                        uint4* dst = reinterpret_cast<uint4*>(to + grow * D);
+#pragma unroll
+                        for (int v4 = 0; v4 < 4; ++v4)
+                            dst[4 * g + v4] = make_uint4(w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2], w[4 * v4 + 3]);
+                    };
+                    uint32_t pkd[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pkd[e] = ptx::pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
+                    if (real) store(p.out, pkd);
+                    if (!CACHE && p.out_lo) {  // what the rounding took: exact in fp32, rounded once
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pkd[e] = ptx::pack_bf16x2(
+                                fmaf(__uint_as_float(ov[2 * e]), inv_l, -__uint_as_float(pkd[e] << 16)),
+                                fmaf(__uint_as_float(ov[2 * e + 1]), inv_l, -__uint_as_float(pkd[e] & 0xffff0000u)));
+                        if (real) store(p.out_lo, pkd);
+                    }
+                }
+            }
+        } else if (!*abort) {
+            record_abort(abort, p.status);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::NCOLS);
+    }
+}
+
+// Joins the partial results of a split call: out = sum_s w_s o_s / sum_s w_s with
+// w_s = 2^(l_s - max l). One warp per query row.
+template <int D>
+__global__ void __launch_bounds__(256) skiparse_frames_join_kernel(const FramesFwdParams p) {
+    const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (row >= p.nrows) return;
+    const long long per_b = static_cast<long long>(p.g.T) * p.g.H * p.g.W * p.g.heads;
+    const int start = p.cache.start[row / per_b];
+    if (start < 0 || start > kMaxStart) return;
+    const float* l = p.part_l + row * p.splits;
+    float m = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, l[s]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    constexpr int PER = D / 32;
+    float acc[PER] = {}, total = 0.f;
+    if (m != -INFINITY) {
+        for (int s = 0; s < p.splits; ++s) {
+            const float w = ptx::ex2_approx(l[s] - m);
+            total += w;
+            const float* o = p.part_o + (row * p.splits + s) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+        }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+        p.out[row * D + lane * PER + e] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
+    if (lane == 0 && p.lse) p.lse[row] = total == 0.f ? -INFINITY : (m + ptx::lg2_approx(total)) * 0.6931471805599453f;
+}
+
+int max_class_tokens(const Geometry& g) {
+    int n = 0;
+    for (int ci = 0; ci < g.Ph; ++ci)
+        for (int cj = 0; cj < g.Pw; ++cj) n = g.Rc[ci] * g.Sc[cj] > n ? g.Rc[ci] * g.Sc[cj] : n;
+    return n;
+}
+
+template <int D, bool CACHE>
+int launch_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
+    using C = Cfg<D, CACHE>;
+    // per device: the kernel's shared-memory attribute is set (host threads may race here;
+    // setting it twice is harmless, the flag only has to be a race-free read)
+    static std::atomic<int> attr_done_dev[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (dev < 0 || dev >= 64 || !attr_done_dev[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(skiparse_attn_frames_kernel<D, CACHE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::SMEM_BYTES);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
+    }
+    const long long n_max = static_cast<long long>(g.T) * max_class_tokens(g);
+    const dim3 grid(static_cast<unsigned>((n_max + 2 * kBM - 1) / (2 * kBM) * p.splits), g.heads, g.B * g.Ph * g.Pw);
+    skiparse_attn_frames_kernel<D, CACHE><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return static_cast<int>(e);
+    skiparse_frames_join_kernel<D><<<static_cast<unsigned>((p.nrows + 7) / 8), 256, 0, stream>>>(p);
+    return static_cast<int>(cudaGetLastError());
+}
+
+template <int D>
+int launch_kind(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
+    return p.cache.k ? launch_d<D, true>(p, g, stream) : launch_d<D, false>(p, g, stream);
+}
+
+}  // namespace
+
+// Splits of the key range: enough CTAs for one per SM (148) from a call with fewer, as long as
+// each part keeps at least four key tiles. The cache's capacity stands for its length, which
+// only the device knows.
+int cached_splits(const Geometry& g, int cap) {
+    const long long nF = max_class_tokens(g);
+    const long long ctas = (g.T * nF + 2 * kBM - 1) / (2 * kBM) * g.heads * g.B * g.Ph * g.Pw;
+    const long long tiles = (cap * nF + kBN - 1) / kBN;
+    long long s = 148 / ctas;
+    if (s > tiles / 4) s = tiles / 4;
+    return static_cast<int>(s < 1 ? 1 : s);
+}
+
+int launch_frames_fwd(const FramesFwdParams& p, const Geometry& g, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (g.d) {
+        case 32: return launch_kind<32>(p, g, st);
+        case 64: return launch_kind<64>(p, g, st);
+        case 128: return launch_kind<128>(p, g, st);
+        default: return static_cast<int>(cudaErrorInvalidValue);
+    }
+}
+
+}  // namespace skiparse

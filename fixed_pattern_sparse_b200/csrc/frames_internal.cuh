@@ -1,0 +1,124 @@
+// frames_internal.cuh -- parameters and launchers of the frame-aware attention operators: class
+// attention with a learned bias by frame distance (forward and backward), the 8-bit frame cache
+// and attention over it. Geometry, class rule and row maps are those of skiparse_internal.cuh.
+#pragma once
+
+#include <cstdint>
+
+#include "skiparse_internal.cuh"
+
+namespace skiparse {
+
+// The bias of a pair of tokens depends on the distance of their frames, u = clamp(t_q - t_k,
+// -D, D): table[buckets[u + D]][head], the pair being masked where the bucket lies outside
+// [0, NB) or the entry is below kBiasMasked (so -inf and the lowest values of a type mask).
+constexpr int kMaxDist = 255;                     // largest D
+constexpr int kMaxDistEntries = 2 * kMaxDist + 1;
+constexpr float kBiasMasked = -1e30f;
+
+struct FrameBias {
+    const uint16_t* table;  // bf16 (NB, heads); nullptr: no bias and no mask
+    const int* buckets;     // (2D+1)
+    int D, NB;
+};
+
+// Where the dimensions of a call lie; filled from Geometry.
+struct FrameGeom {
+    int T, H, W, heads, Ph, Pw, mode;
+    int Rc[kMaxAxisClasses], Sc[kMaxAxisClasses];
+};
+
+// The e4m3 frame cache of one layer: codes (B*classes, heads, cap, F, d), F the padded tokens
+// of a class in one frame, of which class c uses the first Rc*Sc; scales (e8m0 bytes)
+// (B*classes, heads, cap, NBk), one for every kCacheBlock tokens. Frame t lies in slot t % cap.
+constexpr int kCacheBlock = 64;
+constexpr int kScaleLow = 17;      // scale byte of 2^-110, the smallest a writer stores
+constexpr int kMaxStart = 1 << 30; // frame numbers beyond this skip a sequence, as negative ones do
+
+struct CacheView {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* ks;
+    uint8_t* vs;
+    const int* start;  // (B): frame number of the call's first frame; < 0: sequence skipped
+    int cap, F, NBk;
+};
+
+// Forward: bf16 keys and values (k, v), or the cache (cache.k != nullptr).
+struct FramesFwdParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* out;
+    uint16_t* out_lo; // optional: out's rounding residual (bf16 keys only)
+    float* lse;       // optional
+    float* part_o;    // splits > 1: (rows, splits, d) fp32 normalised partial outputs
+    float* part_l;    // splits > 1: (rows, splits) fp32 partial log2-sum-exp
+    int* status;
+    FrameGeom g;
+    FrameBias bias;
+    CacheView cache;
+    int splits;
+    float scale_log2;
+    unsigned long long wait_limit_ns;
+    int fault;
+    long long nrows;  // (token, head) rows of q: the debug bound
+};
+
+struct FramesBwdParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const uint16_t* out;
+    const uint16_t* out_lo;  // optional
+    const uint16_t* dout;
+    const float* lse;
+    float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo))
+    float* lse2;       // workspace (rows): lse * log2(e), at least kLse2Low
+    float* bias2;      // workspace (heads, 2D+1): bias * log2(e), -inf where masked
+    float* part;       // workspace (heads, seqs, tiles, ND): sums of dS by frame distance
+    uint16_t* dtable;  // bf16 (NB, heads)
+    uint16_t* dq;
+    uint16_t* dk;
+    uint16_t* dv;
+    int* status;
+    FrameGeom g;
+    FrameBias bias;
+    int Dn, ND;        // distances that occur: [-Dn, Dn], Dn = min(D, T-1), ND = 2 Dn + 1
+    int seqs, tiles;   // B * classes; 128-key tiles of the longest class
+    float scale_log2, scale;
+    unsigned long long wait_limit_ns;
+    long long nrows;
+    int fault;
+};
+// log2-sum-exp that stands for a row without a visible key: its masked scores of -inf still
+// give exp2(-inf) = 0.
+constexpr float kLse2Low = -1e30f;
+
+struct AppendParams {
+    const uint16_t* k;
+    const uint16_t* v;
+    int* status;
+    FrameGeom g;       // g.T: new frames
+    CacheView cache;
+    int nblk;          // blocks of kCacheBlock tokens of the largest class
+    long long nrows;
+};
+
+// Launchers. They return the cudaError_t as int.
+int launch_frames_fwd(const FramesFwdParams& p, const Geometry& g, void* stream);
+int launch_frames_bwd(const FramesBwdParams& p, const Geometry& g, void* stream);
+int launch_cache_append(const AppendParams& p, const Geometry& g, int d, void* stream);
+// Key splits that launch_frames_fwd should be given for a cache call of these sizes (1: no
+// workspace is needed).
+int cached_splits(const Geometry& g, int cap);
+
+inline void fill_frame_geom(FrameGeom& f, const Geometry& g) {
+    f.T = g.T; f.H = g.H; f.W = g.W; f.heads = g.heads; f.Ph = g.Ph; f.Pw = g.Pw; f.mode = g.mode;
+    for (int c = 0; c < kMaxAxisClasses; ++c) {
+        f.Rc[c] = g.Rc[c];
+        f.Sc[c] = g.Sc[c];
+    }
+}
+
+}  // namespace skiparse

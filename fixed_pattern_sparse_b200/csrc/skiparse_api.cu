@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/skiparse.h"
+#include "api_internal.cuh"
 #include "skiparse_internal.cuh"
 
 namespace {
@@ -105,7 +106,32 @@ int* status_ptr() {
     return p;
 }
 
+// A pending fault of `kind`, consumed (one launch) by the entry point it concerns only.
+int take_fault(int kind) {
+    int expected = kind;
+    return g_fault.compare_exchange_strong(expected, 0) ? 1 : 0;
+}
+
 }  // namespace
+
+// What the entry points of other files share with these.
+namespace skiparse {
+namespace api {
+
+int cuda_fail(int err) { return ::cuda_fail(err); }
+int geometry(int dims, int B, int T, int H, int W, int heads, int d, int P, int mode, Geometry& g) {
+    return make_geometry(dims, B, T, H, W, heads, d, P, mode, g);
+}
+int* status_word() { return status_ptr(); }
+long long debug_bound(long long rows) { return checked_bound(rows); }
+int pending_fault(int kind) { return take_fault(kind); }
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+bool ranges_overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
+    return overlaps(a, abytes, b, bbytes);
+}
+
+}  // namespace api
+}  // namespace skiparse
 
 extern "C" {
 
@@ -179,12 +205,6 @@ long long skiparse1d_rearranged_numel(int B, int T, int H, int W, int heads, int
 
 unsigned long long skiparse_set_wait_limit_ns(unsigned long long ns) {
     return g_wait_limit_ns.exchange(ns == 0 ? kDefaultWaitNs : ns);
-}
-
-// A pending fault of `kind`, consumed (one launch) by the entry point it concerns only.
-static int take_fault(int kind) {
-    int expected = kind;
-    return g_fault.compare_exchange_strong(expected, 0) ? 1 : 0;
 }
 
 int skiparse_debug_inject_fault(int kind) {

@@ -20,7 +20,8 @@
  *     is the token's position in its class's sub-grid: r = h div P (token-wise) or
  *     (h div P^2)*P + h mod P (group-wise), and s likewise from w. Padding is at the
  *     bottom/right of each frame.
- *   - Softmax scale is 1/sqrt(d); no causal mask, no dropout, no bias.
+ *   - Softmax scale is 1/sqrt(d); no dropout; no mask and no bias but those by frame distance
+ *     (skiparse2d_attn_relbias_fwd, skiparse2d_attn_cached).
  *   - Ownership: the caller allocates and owns every buffer. The library allocates no device
  *     memory per call. Its device state: one status word per device, and the fixed workspace
  *     of skiparse2d_attn_bwd_noalloc (a static 16 MiB array on every device that loads the
@@ -259,6 +260,142 @@ SKIPARSE_API long long skiparse1d_class_len(int T, int H, int W, int P, int mode
 /* Elements of the Skiparse-1D rearranged tensor, B*P*P*n*heads*d; -1 on invalid arguments. */
 SKIPARSE_API long long skiparse1d_rearranged_numel(int B, int T, int H, int W, int heads, int d,
                                                    int P);
+
+/*
+ * ---- Attention by frame distance: learned bias, masks, and an 8-bit frame cache --------------
+ * The pages attend densely over all T frames of a class. The entry points below add what a model
+ * that learns or streams over frames needs: a bias that depends on the distance of two tokens'
+ * frames, learned by buckets, with its gradient; the masks (frame-causal, windowed) that the
+ * bucket map expresses; and, for frame-by-frame generation, a cache of the earlier frames' keys
+ * and values in 8 bits with the attention that reads it. The class rule, layouts, alignment,
+ * aliasing and error conventions are those of the other entry points; each function exists for
+ * Skiparse-2D and, with the same arguments, for Skiparse-1D.
+ *
+ * Bias. For a query at frame t_q and a key at frame t_k, u = clamp(t_q - t_k, -D, D) with
+ * D = max_distance, 0 <= D <= 255; distances beyond D share the entry at +-D. With
+ * g = buckets[u + D], the score is q.k/sqrt(d) + table[g][head].
+ *   buckets : (2D+1) int32 on the device, 4-byte aligned. A value outside [0, num_buckets) masks
+ *             the pair: -1 for u < 0 is the frame-causal mask, -1 for |u| >= w a window.
+ *   table   : (num_buckets, heads) bf16, 2-byte aligned. An entry below -1e30 (-inf and the type's
+ *             lowest value among them) masks like a bucket outside the range.
+ * A query row without a visible key gives 0, lse -inf, and zero gradients. Masks act on scores:
+ * keys and values at masked places have to be finite, as everywhere else.
+ */
+
+/*
+ * Class attention with the bias, one kernel launch. Arguments as skiparse2d_attn_fwd_lse;
+ *   lse    : (B, T, H, W, heads) fp32, or NULL if no backward pass follows.
+ *   out_lo : (B, T, H, W, heads, d) bf16, or NULL: what rounding out to bf16 took, itself rounded.
+ * Frames that no row of a query tile can see are not read.
+ */
+SKIPARSE_API int skiparse2d_attn_relbias_fwd(const void* q, const void* k, const void* v, const void* table,
+                                             const int* buckets, int num_buckets, int max_distance,
+                                             void* out, void* out_lo, float* lse, int B, int T, int H,
+                                             int W, int heads, int d, int P, int mode,
+                                             skiparse_stream_t stream);
+SKIPARSE_API int skiparse1d_attn_relbias_fwd(const void* q, const void* k, const void* v, const void* table,
+                                             const int* buckets, int num_buckets, int max_distance,
+                                             void* out, void* out_lo, float* lse, int B, int T, int H,
+                                             int W, int heads, int d, int P, int mode,
+                                             skiparse_stream_t stream);
+
+/*
+ * Its backward pass: dq, dk, dv as skiparse2d_attn_bwd, with P from the biased, masked scores, and
+ *   out_lo : the forward's, or NULL. With it D = rowsum(dout o out) keeps the precision that bf16
+ *            takes from out; the error of dtable is then about that of its own rounding, without
+ *            it up to a few times that.
+ *   dtable : (num_buckets, heads) bf16, written entirely: dtable[g][head] = sum of dS over all
+ *            pairs of the batch in bucket g (summed in fp32, rounded once). A masked entry of the
+ *            table and a bucket that no pair falls in get 0. Must not overlap table.
+ *   workspace : device memory of the caller, 256-byte aligned, of at least
+ *            skiparse2d_attn_relbias_bwd_workspace_bytes() bytes; nothing in it needs clearing,
+ *            and nothing in it is used after the call. Calls that can run at the same time (on
+ *            other streams, or as replays of graphs captured separately) need workspaces of
+ *            their own.
+ * Four kernel launches (row statistics, dk/dv, dq, dtable), no atomics on results: deterministic.
+ */
+SKIPARSE_API int skiparse2d_attn_relbias_bwd(const void* q, const void* k, const void* v, const void* out,
+                                             const void* out_lo, const void* dout, const float* lse,
+                                             const void* table, const int* buckets, int num_buckets, int max_distance,
+                                             void* dq, void* dk, void* dv, void* dtable,
+                                             void* workspace, size_t workspace_bytes, int B, int T,
+                                             int H, int W, int heads, int d, int P, int mode,
+                                             skiparse_stream_t stream);
+SKIPARSE_API int skiparse1d_attn_relbias_bwd(const void* q, const void* k, const void* v, const void* out,
+                                             const void* out_lo, const void* dout, const float* lse,
+                                             const void* table, const int* buckets, int num_buckets, int max_distance,
+                                             void* dq, void* dk, void* dv, void* dtable,
+                                             void* workspace, size_t workspace_bytes, int B, int T,
+                                             int H, int W, int heads, int d, int P, int mode,
+                                             skiparse_stream_t stream);
+/* Workspace bytes of the backward pass, for either mode; -1 on invalid arguments. */
+SKIPARSE_API long long skiparse2d_attn_relbias_bwd_workspace_bytes(int B, int T, int H, int W, int heads,
+                                                                   int d, int P, int max_distance);
+SKIPARSE_API long long skiparse1d_attn_relbias_bwd_workspace_bytes(int B, int T, int H, int W, int heads,
+                                                                   int d, int P, int max_distance);
+
+/*
+ * The frame cache of one layer, a ring of `capacity` frames: frame t lies in slot t mod capacity.
+ *   k_cache, v_cache : (B*P*P, heads, capacity, F, d) e4m3 codes, 16-byte aligned;
+ *                      F = skiparse2d_cache_frame_tokens(H, W, P) = (Hp/P)*(Wp/P). A class with
+ *                      fewer real tokens uses the first of its F places, in the class's raster
+ *                      order; the others are never read or written.
+ *   k_scale, v_scale : (B*P*P, heads, capacity, ceil(F/64)) e8m0 bytes (2^(byte-127)): one scale for
+ *                      every 64 tokens of a frame's class and head.
+ *   start            : (B) int32 on the device, 4-byte aligned: the number of frames of each
+ *                      sequence before this call's T frames, so that these are frames
+ *                      [start[b], start[b]+T). A negative value (or one beyond 2^30) marks a
+ *                      sequence without new frames: its cache and its rows of out and lse are left
+ *                      as they were. The caller advances it, once for all layers.
+ * skiparse2d_cache_append quantises k and v, (B, T, H, W, heads, d) bf16, into their slots: a block's
+ * scale is 2^e with the smallest whole e >= -110 for which its values fit +-448 * 2^e; a code is
+ * x / 2^e rounded to nearest even. A block with an infinity or a NaN gets a NaN scale, and what
+ * attends to it becomes NaN. Other writers of the cache keep to finite codes. T <= capacity.
+ * capacity * F <= 2^30.
+ */
+SKIPARSE_API int skiparse2d_cache_append(const void* k, const void* v, const int* start, void* k_cache,
+                                         void* v_cache, void* k_scale, void* v_scale, int B, int T,
+                                         int H, int W, int heads, int d, int P, int mode,
+                                         int capacity, skiparse_stream_t stream);
+SKIPARSE_API int skiparse1d_cache_append(const void* k, const void* v, const int* start, void* k_cache,
+                                         void* v_cache, void* k_scale, void* v_scale, int B, int T,
+                                         int H, int W, int heads, int d, int P, int mode,
+                                         int capacity, skiparse_stream_t stream);
+/* Places of one class and frame in the cache (F above); -1 on invalid arguments. */
+SKIPARSE_API long long skiparse2d_cache_frame_tokens(int H, int W, int P);
+SKIPARSE_API long long skiparse1d_cache_frame_tokens(int H, int W, int P);
+
+/*
+ * Attention of the T newest frames' queries over the cache, which already holds these frames
+ * (append first): keys are the frames [max(0, start[b]+T-capacity), start[b]+T) of the query's
+ * class, or those of them that the bucket map leaves visible.
+ *   q, out  : (B, T, H, W, heads, d) bf16.
+ *   table, buckets : the bias as above, or both NULL for none (every cached frame visible).
+ *   lse     : (B, T, H, W, heads) fp32, or NULL.
+ *   workspace : device memory of the caller, 256-byte aligned, of at least
+ *             skiparse2d_attn_cached_workspace_bytes() bytes (0: may be NULL); as for the backward
+ *             pass, one for each call that can run at the same time.
+ * One kernel launch, or two where the keys of few queries are cut into parts and joined.
+ */
+SKIPARSE_API int skiparse2d_attn_cached(const void* q, const void* k_cache, const void* v_cache,
+                                        const void* k_scale, const void* v_scale, const int* start,
+                                        const void* table, const int* buckets, int num_buckets,
+                                        int max_distance, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, int B, int T, int H, int W, int heads,
+                                        int d, int P, int mode, int capacity,
+                                        skiparse_stream_t stream);
+SKIPARSE_API int skiparse1d_attn_cached(const void* q, const void* k_cache, const void* v_cache,
+                                        const void* k_scale, const void* v_scale, const int* start,
+                                        const void* table, const int* buckets, int num_buckets,
+                                        int max_distance, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, int B, int T, int H, int W, int heads,
+                                        int d, int P, int mode, int capacity,
+                                        skiparse_stream_t stream);
+/* Workspace bytes of the attention over the cache, for either mode; -1 on invalid arguments. */
+SKIPARSE_API long long skiparse2d_attn_cached_workspace_bytes(int B, int T, int H, int W, int heads, int d,
+                                                              int P, int capacity);
+SKIPARSE_API long long skiparse1d_attn_cached_workspace_bytes(int B, int T, int H, int W, int heads, int d,
+                                                              int P, int capacity);
 
 /*
  * Synchronizes `stream`, then returns and clears the current device's error word: SKIPARSE_OK,
