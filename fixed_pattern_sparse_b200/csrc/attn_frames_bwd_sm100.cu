@@ -8,10 +8,11 @@
 // The schedule is that of the unbiased backward pass (attn_bwd_sm100.cu): a key-major kernel for dK
 // and dV and a query-major one for dQ, seven tile products per pair of tiles, no atomics on
 // results. What the bias adds:
-//   * Frames. Within 64 columns of one frame the bias is one number per row: in the query-major
+//   * Frames. Within 32 columns of one frame the bias is one number per row: in the query-major
 //     kernel it joins the row's log-sum-exp in the existing FMA (no instruction per score), in
-//     the key-major one it is added to each column's. Columns of several frames look the bias up
-//     where the frame changes. Streamed tiles that no stationary row can see are skipped.
+//     the key-major one it is added to each column's. A chunk that holds a frame's border
+//     chooses between two; frames of fewer than 32 tokens look the bias up where it changes.
+//     Streamed tiles that no stationary row can see are skipped.
 //   * D. Every row of dS sums to zero over its keys, so an error of D_i enters the bias gradient
 //     through all of the row's keys with one sign. D from the bf16 output would dominate that
 //     gradient's error; the forward can therefore store what rounding its output took (out_lo).
@@ -345,6 +346,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         const float sl2 = p.scale_log2;
         const bool row_real = first + row < n_c;
         const int t_row = dF.div(min(first + row, n_c - 1));
+        const bool one_frame = __all_sync(0xffffffffu, t_row == __shfl_sync(0xffffffffu, t_row, 0));  // of this warp's rows
         // bias of this row and streamed frame f
         auto bias_of = [&](int f) { return __ldg(bias2 + clamp_dist(KV ? f - t_row : t_row - f, dmax)); };
         // Key-major: adds v, this row's sum of dS over queries of frame f, to the warp's table of
@@ -353,14 +355,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         auto add_hist = [&](float v, int f) {
             const int u = clamp_dist(f - t_row, p.Dn) + p.Dn;
             if (!row_real) v = 0.f;
+            if (one_frame) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float other = __shfl_down_sync(0xffffffffu, v, o);
-                const int uo = __shfl_down_sync(0xffffffffu, u, o);
-                if (lane + o < 32 && uo == u) v += other;
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) my_hist[u] += v;
+            } else {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float other = __shfl_down_sync(0xffffffffu, v, o);
+                    const int uo = __shfl_down_sync(0xffffffffu, u, o);
+                    if (lane + o < 32 && uo == u) v += other;
+                }
+                const int before = __shfl_up_sync(0xffffffffu, u, 1);
+                if (lane == 0 || before != u) my_hist[u] += v;
             }
-            const int before = __shfl_up_sync(0xffffffffu, u, 1);
-            if (lane == 0 || before != u) my_hist[u] += v;
             __syncwarp();  // the next addition may come from another lane
         };
         float acc = 0.f;   // sum of dS over the queries of frame f_acc so far
@@ -373,7 +381,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
             const int valid = jend - j0;               // streamed rows in this half (may be <= 0)
             const int f0 = dF.div(j0);
             const int border = (f0 + 1) * nF - j0;     // column where the next frame starts
-            float off = bias_of(f0);
+            const int f1 = dF.div(j0 + 32), border1 = (f1 + 1) * nF - j0 - 32;  // of the second 32 columns
+            const float off0 = bias_of(f0), off1 = bias_of(f1);
             // every wait of a softmax warp is made uniform over the warp: the tcgen05.ld/st below
             // are .sync.aligned and need all 32 lanes
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_X1), j & 1, abort, lim))) {
@@ -403,18 +412,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(bar(C::B_X1FREE));
                 }
-                if (border >= 64) {
+                if (nF >= 32) {  // a frame starts at most once inside 32 columns
 #pragma unroll
-                    for (int e4 = 0; e4 < 16; ++e4) {
-                        float4 l4 = make_float4(row_l2, row_l2, row_l2, row_l2);
-                        if (KV) l4 = reinterpret_cast<const float4*>(col_l)[e4];
-                        pr[4 * e4] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4]), sl2, off - l4.x));
-                        pr[4 * e4 + 1] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4 + 1]), sl2, off - l4.y));
-                        pr[4 * e4 + 2] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4 + 2]), sl2, off - l4.z));
-                        pr[4 * e4 + 3] = ptx::ex2_approx(fmaf(__uint_as_float(xv[4 * e4 + 3]), sl2, off - l4.w));
+                    for (int g = 0; g < 2; ++g) {
+                        const int bg = g ? border1 : border;
+                        const float o0 = g ? off1 : off0;
+                        if (bg >= 32) {
+#pragma unroll
+                            for (int e4 = 0; e4 < 8; ++e4) {
+                                float4 l4 = make_float4(row_l2, row_l2, row_l2, row_l2);
+                                if (KV) l4 = reinterpret_cast<const float4*>(col_l)[8 * g + e4];
+                                const int e = 32 * g + 4 * e4;
+                                pr[e] = ptx::ex2_approx(fmaf(__uint_as_float(xv[e]), sl2, o0 - l4.x));
+                                pr[e + 1] = ptx::ex2_approx(fmaf(__uint_as_float(xv[e + 1]), sl2, o0 - l4.y));
+                                pr[e + 2] = ptx::ex2_approx(fmaf(__uint_as_float(xv[e + 2]), sl2, o0 - l4.z));
+                                pr[e + 3] = ptx::ex2_approx(fmaf(__uint_as_float(xv[e + 3]), sl2, o0 - l4.w));
+                            }
+                        } else {
+                            const float o1 = bias_of((g ? f1 : f0) + 1);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                pr[32 * g + e] = ptx::ex2_approx(fmaf(__uint_as_float(xv[32 * g + e]), sl2,
+                                                                      (e < bg ? o0 : o1) - (KV ? col_l[32 * g + e] : row_l2)));
+                        }
                     }
-                } else {  // a frame starts inside these columns
+                } else {
                     int f = f0, next = border;
+                    float off = off0;
 #pragma unroll
                     for (int e = 0; e < 64; ++e) {
                         if (e == next) {

@@ -9,21 +9,25 @@
 // 128-row tiles, streams 128-key tiles of K and V through shared-memory rings of two slots,
 // S = Q K^T and O += P V run on tcgen05 with S, P and O in TMEM, one thread per query row does
 // the online softmax with the lazy rescale. What the frames add:
-//   * The bias is constant over the tokens of a frame, so a key tile inside one frame (all but
-//     one in Rc*Sc/128 tiles of a large latent) needs one table lookup per row and tile, folded
-//     into the softmax's existing FMA: no instruction per score. A tile that crosses a
-//     frame border adds the bias per 32-key chunk, and in the chunk with the border per key.
+//   * The bias is constant over the tokens of a frame, so a key tile inside one frame needs one table
+//     lookup per row, folded into the softmax's existing FMA: no instruction per score. A tile
+//     that holds a frame's border gets its biases by a pass over S in TMEM before the softmax.
 //   * The frames that some row of the CTA can see form a range, from the first and last visible
 //     distance of the table; only its keys are loaded. With a causal map that is half the work.
 //     Query tiles are launched last frame first, so that the longest ones start first.
-//   * Cached keys are e4m3 codes. Three producer warps read them with 16-byte loads one tile
-//     ahead into registers, expand them to bf16 (exactly: the scale is a power of two, see
-//     frames_common.cuh) and store them into the swizzled tile, so the tensor-core side and its
-//     precision are those of bf16 keys at half the cache traffic.
+//   * Cached keys are e4m3 codes. Three producer warps for K and three for V copy them into
+//     a staging buffer, expand them to f16 (one conversion per two codes, exact) and store them
+//     into the swizzled tile; the tensor core then works on f16 operands. A block's scale enters
+//     as 2^(e - ref), ref the largest e among the keys this CTA reads, so that a single power
+//     of two for K (in the softmax's factor) and one for V (in the epilogue) are left: exact while
+//     a code times its factor keeps to f16's normal range, that is for blocks down to 2^-22 of
+//     the largest scale, and within 2^-34 of the largest magnitude below. Q's rows are scaled by a
+//     power of two each into f16, and P is kept as 2^7 p, so that f16 holds every p above 2^-31:
+//     P's rounding is 2^-11 instead of bf16's 2^-8.
 //   * Few query tiles over a long cache leave SMs idle: the key range is then cut into `splits`
 //     parts, each CTA writes its normalised partial output and log-sum-exp in fp32, and
 //     a second kernel joins them.
-// Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB.
+// Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB, staging 32 KB.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,24 +41,28 @@ namespace {
 constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kProdWarp0 = 8;
+constexpr int kMaxSmem = 232448;      // 227 KB, the most a CTA may have
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by more than 2^8
+constexpr float kPShift = 7.f;        // cache: P is kept as 2^7 p in f16 (p <= 2^8, 2^15 < 65504)
 constexpr int kPParts = 2;            // P is released to the tensor core in two halves of the key tile
 
 template <int D, bool CACHE>
 struct Cfg : TileGeom<D> {
     using G = TileGeom<D>;
     using G::TILE_BYTES;
-    static constexpr int PROD_WARPS = CACHE ? 3 : 2;
-    static constexpr int MMA_WARP = kProdWarp0 + PROD_WARPS;
+    // bf16: producers 8-9, MMA 10. Cache: producers of K 8-10 and of V 12-14, MMA 15, so that the
+    // MMA issuer's sub-partition has no producer; 11 idles.
+    static constexpr int MMA_WARP = CACHE ? 15 : kProdWarp0 + 2;
     static constexpr int THREADS = 32 * (MMA_WARP + 1);
-    static constexpr int FULL_COUNT = CACHE ? PROD_WARPS : 32 * PROD_WARPS;  // arrivals per tile
+    static constexpr int FULL_COUNT = CACHE ? 3 : 64;  // arrivals per tile
     static constexpr int KST = 2, VST = 2;
     static constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_O0 = 256, COL_O1 = 256 + D;
     static constexpr uint32_t NCOLS = 512;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = 2 * TILE_BYTES;
     static constexpr int OFF_V = OFF_K + KST * TILE_BYTES;
-    static constexpr int OFF_TAB = OFF_V + VST * TILE_BYTES;  // bias by distance index
+    static constexpr int OFF_STAGE = OFF_V + VST * TILE_BYTES;  // cache: a tile of codes of K and of V
+    static constexpr int OFF_TAB = OFF_STAGE + (CACHE ? 2 * kBN * D : 0);  // bias by distance index
     static constexpr int OFF_BAR = OFF_TAB + 4 * (kMaxDistEntries + 1);
     static constexpr int B_Q = 0;
     static constexpr int B_KFULL = 1;
@@ -65,84 +73,208 @@ struct Cfg : TileGeom<D> {
     static constexpr int B_PFULL = B_SFULL + 2;
     static constexpr int B_OFULL = B_PFULL + 2 * kPParts;
     static constexpr int B_DRAIN = B_OFULL + 1;
-    static constexpr int NBARS = B_DRAIN + 1;
+    static constexpr int B_QF16 = B_DRAIN + 1;               // cache: Q has been turned into f16
+    static constexpr int NBARS = B_QF16 + 1;
     static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NBARS;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
     static constexpr int OFF_RANGE = OFF_ABORT + 4;  // first and last visible distance
-    static constexpr int SMEM_USED = OFF_RANGE + 8;
-    // + slack for 1024-byte alignment; at least 116 KB so that one CTA (and its 512 TMEM
-    // columns) owns an SM even for small d
-    static constexpr int SMEM_BYTES = SMEM_USED + 1024 > 118784 ? SMEM_USED + 1024 : 118784;
+    static constexpr int OFF_REF = OFF_RANGE + 8;    // cache: largest scale bytes of K and V
+    static constexpr int SMEM_USED = OFF_REF + 8;
+    // + slack for 1024-byte alignment where it fits (the kernel checks the slack it got); at
+    // least 116 KB so that one CTA (and its 512 TMEM columns) owns an SM even for small d
+    static constexpr int SMEM_BYTES =
+        SMEM_USED + 1024 > kMaxSmem ? kMaxSmem : (SMEM_USED + 1024 > 118784 ? SMEM_USED + 1024 : 118784);
     static_assert(COL_O1 + D <= NCOLS, "TMEM overflow");
-    static_assert(SMEM_BYTES <= 232448, "shared memory overflow");
+    static_assert(SMEM_USED + 256 <= kMaxSmem, "shared memory overflow");
 };
 
-// The rows of a 128-key tile that one producer lane expands: 16 codes (one 16-byte chunk) of
-// every third row group of its warp.
+// Instruction descriptor of kind::f16 with f16 (instead of bf16) A and B.
+constexpr uint32_t f16_operands(uint32_t idesc) { return idesc & ~((1u << 7) | (1u << 10)); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One producer lane's part of the tiles of codes of K or V: a 16-byte chunk (16 codes) of every third
+// row group. The chunks travel by cp.async through a staging buffer in shared memory that only
+// the lane itself reads, the scale bytes through registers.
 template <int D>
 struct CacheTile {
     static constexpr int CPR = D / 16;            // chunks per row of codes
     static constexpr int RPI = 32 / CPR;          // rows per warp instruction
     static constexpr int NG = kBN / RPI;          // row groups of a tile
     static constexpr int PER = (NG + 2) / 3;      // row groups of a warp
-    uint4 x[PER];
-    uint32_t sc[PER];
+    static constexpr int STAGE_BYTES = NG * 512;  // a tile of codes
+    uint32_t byte[PER < 3 ? 3 : PER];             // scale bytes
+    int at0;                                      // of the tile whose bytes these are: its first token's
+    bool inside;                                  // place in its frame, and whether it lies in one
+    const uint8_t* codes;                         // of this (subsequence, head)
+    const uint8_t* scales;
+    uint32_t stage;                               // this lane's first chunk
+    int pw, lane;
 
-    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int j0,
-                                         int jend, const FastDiv& dF, int nF, int F, int NBk, int cap, int pw, int lane,
-                                         int* status) {
+    static __device__ __forceinline__ bool mine(int i, int pw) { return 3 * i + 2 < NG || pw + 3 * i < NG; }
+    __device__ __forceinline__ void init(const uint8_t* codes_, const uint8_t* scales_, uint32_t stage_base, int pw_, int lane_) {
+        codes = codes_;
+        scales = scales_;
+        pw = pw_;
+        lane = lane_;
+        stage = stage_base + pw * 512 + lane * 16;
+    }
+    // Starts the copies of the keys j0..j0+127 of the class, those from jend on repeating the last.
+    __device__ __forceinline__ void fetch(int j0, int jend, const FastDiv& dF, int nF, const CacheView& cv, int* status) const {
         const int c = lane % CPR, rsub = lane / CPR;
+        const int slot0 = dF.div(j0), at0 = j0 - slot0 * nF;
+        const long long rows = static_cast<long long>(cv.cap) * cv.F;
+        if (at0 + kBN <= nF && j0 + kBN <= jend) {  // inside one frame: constant strides
+            const long long row0 = load_row(static_cast<long long>(slot0) * cv.F + at0 + pw * RPI + rsub, rows, status);
+            const uint8_t* src = codes + row0 * D + c * 16;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int g = pw + 3 * i;
-            if (g < NG) {
-                const int j = min(j0 + g * RPI + rsub, jend - 1);  // rows past the end repeat the last one
-                const int slot = dF.div(j), at = j - slot * nF;
-                const long long row = load_row(static_cast<long long>(slot) * F + at,
-                                               static_cast<long long>(cap) * F, status);
-                x[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * D) + c);
-                sc[i] = __ldg(scales + static_cast<long long>(slot) * NBk + at / kCacheBlock);
-            }
+            for (int i = 0; i < PER; ++i)
+                if (mine(i, pw)) cp_async_16(stage + i * 3 * 512, src + i * 3 * RPI * D);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (mine(i, pw)) {
+                    const int j = min(j0 + (pw + 3 * i) * RPI + rsub, jend - 1);
+                    const int slot = dF.div(j), at = j - slot * nF;
+                    const long long row = load_row(static_cast<long long>(slot) * cv.F + at, rows, status);
+                    cp_async_16(stage + i * 3 * 512, codes + row * D + c * 16);
+                }
+        }
+        cp_async_commit();
+    }
+    // Loads the scale bytes of the same rows: of a tile inside one frame the three that it can meet.
+    __device__ __forceinline__ void fetch_scales(int j0, int jend, const FastDiv& dF, int nF, const CacheView& cv) {
+        const int slot0 = dF.div(j0);
+        at0 = j0 - slot0 * nF;
+        inside = at0 + kBN <= nF && j0 + kBN <= jend;
+        if (inside) {
+            const uint8_t* sc = scales + static_cast<long long>(slot0) * cv.NBk;
+            const int last = (at0 + kBN - 1) / kCacheBlock;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) byte[i] = __ldg(sc + min(at0 / kCacheBlock + i, last));
+        } else {
+            const int rsub = lane / CPR;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (mine(i, pw)) {
+                    const int j = min(j0 + (pw + 3 * i) * RPI + rsub, jend - 1);
+                    const int slot = dF.div(j), at = j - slot * nF;
+                    byte[i] = __ldg(scales + static_cast<long long>(slot) * cv.NBk + at / kCacheBlock);
+                }
         }
     }
-    __device__ __forceinline__ void store(uint32_t dst, int pw, int lane) const {
+    // Whether every scale of the warp's rows is the reference; if not, byte[] is filled row by row.
+    __device__ __forceinline__ bool all_ref(int ref) {
+        const uint32_t r = static_cast<uint32_t>(ref);
+        if (inside) {
+            const uint32_t b0 = byte[0], b1 = byte[1], b2 = byte[2];
+            if (b0 == r && b1 == r && b2 == r) return true;
+            const int r0 = at0 % kCacheBlock + pw * RPI + lane / CPR;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int blk = (r0 + 3 * i * RPI) / kCacheBlock;
+                byte[i] = blk == 0 ? b0 : blk == 1 ? b1 : b2;
+            }
+            return false;
+        }
+        bool one = true;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (mine(i, pw)) one = one && byte[i] == r;
+        return __all_sync(0xffffffffu, one);
+    }
+    // Expands the staged tile into the swizzled f16 tile at dst, times 2^(scale - ref).
+    template <bool SCALED>
+    __device__ __forceinline__ void expand(uint32_t dst, int ref) const {
         using C = TileGeom<D>;
         const int c = lane % CPR, rsub = lane / CPR;
-        const uint32_t box = static_cast<uint32_t>(c * 32) / C::SW;
-        const uint32_t cb = static_cast<uint32_t>(c * 32) % C::SW / 16;
+        // A chunk gives two 16-byte stores; the lanes of a row's second box start with their second
+        // half, so that the lanes of a row never meet in a bank. The rows of a lane are 3 * RPI
+        // apart: their swizzles repeat after two (D = 128) or do not change.
+        const int flip = (c * 32 / C::SW) & 1;
+        const int r0 = pw * RPI + rsub;
+        const uint32_t even[2] = {dst + tile_chunk<D>(r0, 2 * c + flip), dst + tile_chunk<D>(r0, 2 * c + 1 - flip)};
+        const uint32_t odd[2] = {dst + tile_chunk<D>(r0 + 3 * RPI, 2 * c + flip) - 3 * RPI * C::SW,
+                                 dst + tile_chunk<D>(r0 + 3 * RPI, 2 * c + 1 - flip) - 3 * RPI * C::SW};
+        const uint32_t half_at[2] = {stage + 8 * flip, stage + 8 - 8 * flip};
+        // loads in batches, ahead of the conversions that use them
+        constexpr int BATCH = 4;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int g = pw + 3 * i;
-            if (g < NG) {
-                const int r = g * RPI + rsub;
-                const uint32_t m = scale_mul(sc[i]);
-                uint32_t y[8];
-                e4m3x4_to_bf16(x[i].x, m, y[0], y[1]);
-                e4m3x4_to_bf16(x[i].y, m, y[2], y[3]);
-                e4m3x4_to_bf16(x[i].z, m, y[4], y[5]);
-                e4m3x4_to_bf16(x[i].w, m, y[6], y[7]);
-                if (__any_sync(0xffffffffu, sc[i] > 134u)) {  // magnitudes beyond 57344
-                    const uint32_t rest = scale_rest(sc[i]);
+        for (int i0 = 0; i0 < PER; i0 += BATCH) {
+            uint32_t w[2 * BATCH][2];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = bf16x2_mul(y[e], rest);
+            for (int i = i0; i < i0 + BATCH && i < PER; ++i)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (mine(i, pw))
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                     : "=r"(w[2 * (i - i0) + half][0]), "=r"(w[2 * (i - i0) + half][1])
+                                     : "r"(half_at[half] + i * 3 * 512));
+#pragma unroll
+            for (int i = i0; i < i0 + BATCH && i < PER; ++i)
+                if (mine(i, pw)) {
+                    uint32_t m = 0;
+                    if (SCALED) m = scale_f16x2(byte[i], ref);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t* c = w[2 * (i - i0) + half];
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            y[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(c[e]));
+                            y[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(c[e] >> 16));
+                        }
+                        if (SCALED) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = f16x2_mul(y[e], m);
+                        }
+                        const uint32_t at = ((i & 1) ? odd[half] : even[half]) + i * 3 * RPI * C::SW;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                                     "r"(y[3])
+                                     : "memory");
+                    }
                 }
-                const uint32_t sw = C::SW == 128 ? static_cast<uint32_t>(r & 7) : static_cast<uint32_t>((r >> 1) & 3);
-                const uint32_t base = dst + box * C::BOX_BYTES + static_cast<uint32_t>(r) * C::SW;
-                // two 16-byte stores; the lanes of a row's second box start with their second
-                // half, so that the eight lanes of a row never meet in a bank
-                const bool flip = box & 1u;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t hi = flip ? 1u - half : half;
-                    const uint32_t a = base + (((cb + hi) ^ sw) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(hi ? y[4] : y[0]),
-                                 "r"(hi ? y[5] : y[1]), "r"(hi ? y[6] : y[2]), "r"(hi ? y[7] : y[3])
-                                 : "memory");
-                }
-            }
         }
     }
 };
+
+// Turns one row of a Q tile in shared memory from bf16 into f16, times the power of two that puts
+// the row's largest magnitude in [2^7, 2^8): exact for values down to 2^-22 of it, within 2^-33 of
+// it below. Returns that power's exponent (the row is 2^exponent times what is stored).
+template <int D>
+__device__ __forceinline__ int q_row_to_f16(uint32_t tile, int row) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(tile + tile_chunk<D>(row, c)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __vmaxu2(top, v[e] & 0x7fff7fffu);
+    }
+    top = max(top & 0xffffu, top >> 16);
+    const int up = top == 0 ? 0 : max(static_cast<int>(top >> 7), 8) - 134;  // 127 + 7
+    const float f = exp2_int(-up);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        const uint32_t at = tile + tile_chunk<D>(row, c);
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(at));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = pack_f16x2(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
+    }
+    return up;
+}
 
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frames_kernel(const FramesFwdParams p) {
@@ -174,6 +306,12 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+    if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {
+        // the dynamic shared memory is not aligned well enough for this layout (uniform over the
+        // CTA, before any shared state): report it instead of running out of bounds
+        if (threadIdx.x == 0) atomicExch(p.status, kErrLaunch);
+        return;
+    }
     uint8_t* smem = smem_raw + pad;
     const uint32_t sbase = raw_base + pad;
     auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
@@ -181,6 +319,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
     float* tab = reinterpret_cast<float*>(smem + C::OFF_TAB);
     int* range = reinterpret_cast<int*>(smem + C::OFF_RANGE);
+    int* refs = reinterpret_cast<int*>(smem + C::OFF_REF);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -207,7 +346,9 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         }
         ptx::mbar_init(bar(C::B_OFULL), 1);
         ptx::mbar_init(bar(C::B_DRAIN), 1);
+        ptx::mbar_init(bar(C::B_QF16), 2 * kBM);
         *abort = 0;
+        refs[0] = refs[1] = 0;
         range[0] = dmax + 1;
         range[1] = -dmax - 1;
         ptx::fence_mbar_init();
@@ -253,11 +394,42 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int jend = (f_hi + 1) * nF;                          // end of the visible keys
     const int jbeg = f_lo * nF + split * per_split * kBN;      // this CTA's first key
     const int nkv = max(0, min(per_split, nkv_all - split * per_split));
+    // cache: the largest scale among the keys read. Codes enter the tensor core as f16 values
+    // code * 2^(e - ref), so that one power of two for K and one for V remain to be applied.
+    const long long sh = static_cast<long long>(seq) * p.g.heads + head;
+    const uint8_t* k_scales = CACHE ? p.cache.ks + sh * p.cache.cap * p.cache.NBk : nullptr;
+    const uint8_t* v_scales = CACHE ? p.cache.vs + sh * p.cache.cap * p.cache.NBk : nullptr;
+    if (CACHE && nkv > 0) {
+        const int s_lo = dF.div(jbeg), s_hi = dF.div(min(jbeg + nkv * kBN, jend) - 1);
+        const int used = (nF + kCacheBlock - 1) / kCacheBlock, count = (s_hi - s_lo + 1) * used;
+        int kr = 0, vr = 0;
+        for (int i = threadIdx.x; i < count; i += C::THREADS) {
+            const long long at = static_cast<long long>(s_lo + i / used) * p.cache.NBk + i % used;
+            const int kb = __ldg(k_scales + at), vb = __ldg(v_scales + at);
+            kr = max(kr, kb == 255 ? 0 : kb);
+            vr = max(vr, vb == 255 ? 0 : vb);
+        }
+        kr = __reduce_max_sync(0xffffffffu, kr);
+        vr = __reduce_max_sync(0xffffffffu, vr);
+        if (lane == 0) {
+            atomicMax(&refs[0], kr);
+            atomicMax(&refs[1], vr);
+        }
+        __syncthreads();
+    }
 
+    if (CACHE) {
+        // 512 threads start with 128 registers each; the softmax needs 168: 2 * 168 + 2 * 88 = 4 * 128
+        if (warp < kProdWarp0)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    }
     if (warp >= kProdWarp0) {
         if (warp < C::MMA_WARP) {
             // ------------------------------------------------------------------ producers
-            const int pw = warp - kProdWarp0;
+            const bool of_v = warp >= 12;                       // cache: K by warps 8-10, V by 12-14
+            const int pw = warp - (of_v ? 12 : kProdWarp0);
             const int fault_skip = (p.fault == 1 && pw == 0 && lane == 0);
             bool ok = true;
             auto wait_empty = [&](bool is_v, int j) {  // the slot of key step j is free
@@ -268,34 +440,38 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     w_ok = ptx::mbar_wait(bar((is_v ? C::B_VEMPTY : C::B_KEMPTY) + j % nst), ((j / nst) - 1) & 1, abort, lim);
                 return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
             };
-            if (nkv > 0 && pw < 2) {
+            if (nkv > 0 && pw < 2 && !of_v) {
                 load_tile<D>(sbase + C::OFF_Q, p.q, rows, q_first, n_q, pw, lane, p.nrows, p.status);
                 load_tile<D>(sbase + C::OFF_Q + C::TILE_BYTES, p.q, rows, q_first + kBM, n_q, pw, lane, p.nrows, p.status);
                 cp_async_arrive_noinc(bar(C::B_Q));
             }
             if constexpr (CACHE) {
-                const long long sh = static_cast<long long>(seq) * p.g.heads + head;
-                const long long code0 = sh * p.cache.cap * p.cache.F * D, scale0 = sh * p.cache.cap * p.cache.NBk;
-                CacheTile<D> kt, vt;
-                auto load = [&](CacheTile<D>& t, const uint8_t* codes, const uint8_t* scales, int j) {
-                    t.load(codes + code0, scales + scale0, jbeg + j * kBN, jend, dF, nF, p.cache.F, p.cache.NBk, p.cache.cap,
-                           pw, lane, p.status);
+                static_assert(C::KST == C::VST, "one slot index for both rings");
+                CacheTile<D> t;
+                t.init((of_v ? p.cache.v : p.cache.k) + sh * p.cache.cap * p.cache.F * D, of_v ? v_scales : k_scales,
+                       sbase + C::OFF_STAGE + (of_v ? CacheTile<D>::STAGE_BYTES : 0), pw, lane);
+                const int ref = refs[of_v];
+                const uint32_t ring = sbase + (of_v ? C::OFF_V : C::OFF_K);
+                auto fetch = [&](int j) {
+                    t.fetch_scales(jbeg + j * kBN, jend, dF, nF, p.cache);
+                    t.fetch(jbeg + j * kBN, jend, dF, nF, p.cache, p.status);
                 };
-                auto release = [&](int full, bool signal) {  // the stores of this warp, for the tensor core
-                    fence_proxy_async();
+                const int steps = pw < 3 ? nkv : 0;
+                if (steps > 0) fetch(0);
+                for (int j = 0; j < steps; ++j) {
+                    cp_async_wait<0>();
+                    if (!(ok = wait_empty(of_v, j))) break;
+                    const uint32_t dst = ring + (j % C::KST) * C::TILE_BYTES;
+                    if (t.all_ref(ref))
+                        t.template expand<false>(dst, ref);
+                    else
+                        t.template expand<true>(dst, ref);
+                    fence_proxy_async();  // these stores, for the tensor core
                     __syncwarp();
-                    if (lane == 0 && signal) ptx::mbar_arrive(bar(full));
-                };
-                if (nkv > 0) load(kt, p.cache.k, p.cache.ks, 0);
-                for (int j = 0; j < nkv; ++j) {
-                    load(vt, p.cache.v, p.cache.vs, j);
-                    if (!(ok = wait_empty(false, j))) break;
-                    kt.store(sbase + C::OFF_K + (j % C::KST) * C::TILE_BYTES, pw, lane);
-                    release(C::B_KFULL + j % C::KST, !(fault_skip && j == 0));  // test hook: one warp never signals
-                    if (j + 1 < nkv) load(kt, p.cache.k, p.cache.ks, j + 1);
-                    if (!(ok = wait_empty(true, j))) break;
-                    vt.store(sbase + C::OFF_V + (j % C::VST) * C::TILE_BYTES, pw, lane);
-                    release(C::B_VFULL + j % C::VST, true);
+                    // test hook: one warp never signals the first K tile
+                    if (lane == 0 && !(fault_skip && !of_v && j == 0))
+                        ptx::mbar_arrive(bar((of_v ? C::B_VFULL : C::B_KFULL) + j % C::KST));
+                    if (j + 1 < steps) fetch(j + 1);
                 }
             } else {
                 TileRows kv{0, 0};  // token rows of key step j, shared by its K and V tiles
@@ -316,8 +492,9 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         } else {
             // ------------------------------------------------------------------ MMA issuer
             if (lane == 0 && nkv > 0) {
-                const uint32_t idesc_s = ptx::idesc_bf16_f32(kBM, kBN, false);
-                const uint32_t idesc_o = ptx::idesc_bf16_f32(kBM, D, true);
+                constexpr uint32_t bf16_s = ptx::idesc_bf16_f32(kBM, kBN, false), bf16_o = ptx::idesc_bf16_f32(kBM, D, true);
+                constexpr uint32_t idesc_s = CACHE ? f16_operands(bf16_s) : bf16_s;
+                constexpr uint32_t idesc_o = CACHE ? f16_operands(bf16_o) : bf16_o;
                 const uint32_t q0 = sbase + C::OFF_Q, q1 = q0 + C::TILE_BYTES;
                 const uint64_t qd0 = ptx::smem_desc(q0, 16, 8 * C::SW, C::LAYOUT);
                 const uint64_t qd1 = ptx::smem_desc(q1, 16, 8 * C::SW, C::LAYOUT);
@@ -348,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     }
                     return true;
                 };
-                bool ok = ptx::mbar_wait(bar(C::B_Q), 0, abort, lim) &&
+                bool ok = ptx::mbar_wait(bar(CACHE ? C::B_QF16 : C::B_Q), 0, abort, lim) &&
                           ptx::mbar_wait(bar(C::B_KFULL + 0), 0, abort, lim);
                 if (ok) {
                     fence_proxy_async();  // cp.async data observed through the barriers, for the MMA
@@ -410,20 +587,29 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         const uint32_t s_addr = tmem + lane_base + (qt ? C::COL_S1 : C::COL_S0);
         const uint32_t o_col = qt ? C::COL_O1 : C::COL_O0;
         const uint32_t sfull = bar(C::B_SFULL + qt);
-        const float sl2 = p.scale_log2;
         const int qi = q_first + qt * kBM + row;
         const int tq = start + dF.div(min(qi, n_q - 1));
         auto bias_of = [&](int f) { return tab[clamp_dist(tq - frame_time(f), dmax) + dmax]; };
         float m_run = -INFINITY, l_run = 0.f;  // in units of log2
         bool ok = true;
-        for (int j = 0; j < nkv; ++j) {
+        float sl2 = p.scale_log2;
+        if (CACHE && nkv > 0) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_Q), 0, abort, lim));
+            if (ok) {
+                const int up = q_row_to_f16<D>(sbase + C::OFF_Q + qt * C::TILE_BYTES, row);
+                sl2 *= exp2_int(up + refs[0] - 127);
+                fence_proxy_async();
+                ptx::mbar_arrive(bar(C::B_QF16));
+            }
+        }
+        for (int j = 0; ok && j < nkv; ++j) {
             // Every wait of a softmax warp is made uniform over the warp (a lane can see the abort
             // flag while another sees the phase complete): the tcgen05.ld/st below are
             // .sync.aligned and need all 32 lanes.
             const int j0 = jbeg + j * kBN;
             const int f0 = dF.div(j0);
             const int border = (f0 + 1) * nF - j0;  // tile column where the next frame starts
-            float off = bias_of(f0), mul = sl2;
+            float off = bias_of(f0), mul = sl2;     // scores are S * mul + off, in log2
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(sfull, j & 1, abort, lim))) {
                 ok = false;
                 break;
@@ -431,22 +617,33 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             ptx::tc_fence_after();
             if (border < kBN) {
                 // A frame starts inside the tile: S becomes S * scale + bias in place, 32 columns at
-                // a time, before the softmax below reads the row. `next` is the column (in this
-                // chunk) where the bias changes next.
-                int f = f0, next = border;
+                // a time, before the softmax below reads the row. (Biases per chunk carried through
+                // the softmax instead cost the tiles without a border 18 %.)
+                int f = f0, next = border;          // column of this chunk where the next frame starts
 #pragma unroll 1
                 for (int g = 0; g < 4; ++g) {
                     uint32_t sv[32];
                     ptx::tmem_ld32(s_addr + 32 * g, sv);
                     ptx::tmem_wait_ld();
+                    if (next >= 32) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (e == next) {
-                            ++f;
-                            next += nF;
-                            off = bias_of(f);  // columns past the last frame are masked below
+                        for (int e = 0; e < 32; ++e) sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, off));
+                    } else if (nF >= 32) {          // one border
+                        const float o1 = bias_of(++f);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, e < next ? off : o1));
+                        off = o1;
+                        next += nF;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (e == next) {
+                                next += nF;
+                                off = bias_of(++f);  // columns past the last frame are masked below
+                            }
+                            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, off));
                         }
-                        sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, off));
                     }
                     next -= 32;
                     ptx::tmem_st16(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
@@ -494,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             // P = 2^(S*scale*log2(e) + bias - m), written as bf16 pairs over the first 64 columns of
             // S, in two halves released as they are stored. A row that has seen no key yet keeps
             // the reference 0, so that its -inf scores give 0.
-            const float neg = off - (m_run == -INFINITY ? 0.f : m_run);
+            const float neg = off - (m_run == -INFINITY ? 0.f : m_run) + (CACHE ? kPShift : 0.f);
             float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;  // four short addition chains
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -512,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                         sum0 += p0;
                         sum1 += p1;
                     }
-                    pk[e] = ptx::pack_bf16x2(p0, p1);
+                    pk[e] = CACHE ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
                 }
                 ptx::tmem_st16(s_addr + 16 * g, pk);
                 if (g == 1 && j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -542,8 +739,9 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         if (ok && (nkv == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_OFULL), 0, abort, lim)))) {
             ptx::tc_fence_after();
             // a row without a visible key: 0, and -inf for its log-sum-exp
-            const float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;
-            const float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run);
+            const float v_scale = CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f;
+            const float inv_l = l_run == 0.f ? 0.f : v_scale / l_run;
+            const float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run) - (CACHE ? kPShift : 0.f);
             const bool real = qi < n_q && row_ok(rows(qi), p.nrows, p.status);
             const size_t grow = real ? static_cast<size_t>(rows(qi)) : 0;
             if (real) {
@@ -658,6 +856,12 @@ int launch_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
         e = cudaFuncSetAttribute(skiparse_attn_frames_kernel<D, CACHE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::SMEM_BYTES);
         if (e != cudaSuccess) return static_cast<int>(e);
+        if (CACHE) {  // the kernel's register split counts on what it was compiled with
+            cudaFuncAttributes a;
+            e = cudaFuncGetAttributes(&a, skiparse_attn_frames_kernel<D, CACHE>);
+            if (e != cudaSuccess) return static_cast<int>(e);
+            if (a.numRegs != 128) return static_cast<int>(cudaErrorInvalidConfiguration);
+        }
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
     const long long n_max = static_cast<long long>(g.T) * max_class_tokens(g);

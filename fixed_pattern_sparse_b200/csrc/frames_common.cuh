@@ -24,31 +24,35 @@ __device__ __forceinline__ float bias_log2(const FrameBias& fb, int heads, int u
 
 __device__ __forceinline__ int clamp_dist(int u, int D) { return min(max(u, -D), D); }
 
-// The four e4m3 codes of a word as bf16, times a power of two m (as a bf16 pair): an e4m3 code's
-// exponent and mantissa, moved to the low bits of bf16's fields, are its value times 2^-120 (a
-// subnormal code becomes a bf16 subnormal), so with m = 2^(120 + e) the product is code * 2^e,
-// exactly: three mantissa bits fit bf16's seven.
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+// e4m3 codes as f16 pairs: every code is an f16 value exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3_pair_raw(uint32_t x) {  // codes in bytes 1 and 3 of x
-    return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t m, uint32_t& lo, uint32_t& hi) {
-    lo = bf16x2_mul(e4m3_pair_raw(__byte_perm(w, 0u, 0x1404)), m);
-    hi = bf16x2_mul(e4m3_pair_raw(__byte_perm(w, 0u, 0x3424)), m);
+// 2^(byte - ref) as an f16 pair, byte <= ref: exact down to 2^-24, 0 below; NaN for byte 255.
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte, int ref) {
+    const int down = ref - static_cast<int>(byte);
+    uint32_t h = down <= 14 ? static_cast<uint32_t>(15 - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;
+    if (byte == 255u) h = 0x7e00u;
+    return h | (h << 16);
 }
-// The bf16 pair 2^(120 + e) of a scale byte e + 127, for e <= 7; beyond, the largest power, and
-// the caller multiplies by scale_rest() too. 255 is NaN.
-__device__ __forceinline__ uint32_t scale_mul(uint32_t byte) {
-    const uint32_t f = byte >= 255u ? 0x7fc0u : (min(byte, 134u) + 120u) << 7;
-    return f | (f << 16);
+// 2^e in fp32, e clamped to its normal range.
+__device__ __forceinline__ float exp2_int(int e) {
+    return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 127) + 127) << 23);
 }
-__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
-    const uint32_t f = byte > 134u ? (byte - 134u + 127u) << 7 : 127u << 7;
-    return (f | (f << 16)) & 0x7fff7fffu;
+// Byte offset of 16-byte chunk c of row r in a tile of TileGeom<D>'s swizzled layout.
+template <int D>
+__device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
+    using C = TileGeom<D>;
+    const uint32_t box = static_cast<uint32_t>(c * 16) / C::SW, cb = static_cast<uint32_t>(c * 16) % C::SW / 16;
+    const uint32_t sw = C::SW == 128 ? static_cast<uint32_t>(r & 7) : static_cast<uint32_t>((r >> 1) & 3);
+    return box * C::BOX_BYTES + static_cast<uint32_t>(r) * C::SW + ((cb ^ sw) << 4);
 }
 
 }  // namespace skiparse
