@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libskiparse.so")
 DEBUG_LIB = os.path.join(HERE, "libskiparse_debug.so")
 SOURCES = ["skiparse_api.cu", "attn_fwd_sm100.cu", "attn_bwd_sm100.cu", "rearrange.cu", "no_alloc.cu",
            "host_pipeline.cu", "diag_sm100.cu", "frames_api.cu", "cache_append.cu", "attn_frames_fwd_sm100.cu",
-           "attn_frames_bwd_sm100.cu"]
+           "attn_frames_bwd_sm100.cu", "attn_cached_small.cu"]
 HEADERS = ["ptx_sm100.cuh", "skiparse_internal.cuh", "attn_common.cuh", "api_internal.cuh", "frames_internal.cuh",
            "frames_common.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

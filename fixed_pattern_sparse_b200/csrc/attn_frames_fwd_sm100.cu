@@ -43,7 +43,6 @@ constexpr int kBN = 128;
 constexpr int kProdWarp0 = 8;
 constexpr int kMaxSmem = 232448;      // 227 KB, the most a CTA may have
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by more than 2^8
-constexpr float kPShift = 7.f;        // cache: P is kept as 2^7 p in f16 (p <= 2^8, 2^15 < 65504)
 constexpr int kPParts = 2;            // P is released to the tensor core in two halves of the key tile
 
 template <int D, bool CACHE>
@@ -90,12 +89,6 @@ struct Cfg : TileGeom<D> {
 
 // Instruction descriptor of kind::f16 with f16 (instead of bf16) A and B.
 constexpr uint32_t f16_operands(uint32_t idesc) { return idesc & ~((1u << 7) | (1u << 10)); }
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // One producer lane's part of the tiles of codes of K or V: a 16-byte chunk (16 codes) of every third
 // row group. The chunks travel by cp.async through a staging buffer in shared memory that only
@@ -295,13 +288,8 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         start = p.cache.start[b];
         if (start < 0 || start > kMaxStart) return;  // a sequence without new frames
     }
-    const int end = start + p.g.T;                  // frames up to the newest query's
-    const bool wrapped = CACHE && end > p.cache.cap;  // every slot of the ring is in use
-    const int nframes = wrapped ? p.cache.cap : end;  // frames (slots) that hold keys
-    // frame of slot f: f + fbase, one turn of the ring earlier beyond the newest slot
-    const int fnew = wrapped ? (end - 1) % p.cache.cap : nframes;
-    const int fbase = wrapped ? end - 1 - fnew : 0;
-    auto frame_time = [&](int f) { return f + fbase - (f > fnew ? p.cache.cap : 0); };
+    FrameRing ring;
+    ring.init(start + p.g.T, CACHE ? p.cache.cap : p.g.T);
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
@@ -358,15 +346,8 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         ptx::tmem_relinquish();
     }
     // the bias by distance, and the first and last distance that is visible
-    int dlo = dmax + 1, dhi = -dmax - 1;
-    for (int u = threadIdx.x; u <= 2 * dmax; u += C::THREADS) {
-        const float v = bias_log2(p.bias, p.g.heads, u, head);
-        tab[u] = v;
-        if (v != -INFINITY) {
-            dlo = min(dlo, u - dmax);
-            dhi = max(dhi, u - dmax);
-        }
-    }
+    int dlo, dhi;
+    fill_bias(tab, p.bias, p.g.heads, head, C::THREADS, dlo, dhi);
     ptx::tc_fence_before();
     __syncthreads();
     dlo = __reduce_min_sync(0xffffffffu, dlo);
@@ -380,15 +361,8 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const uint32_t tmem = *tmem_slot;
     dlo = range[0];
     dhi = range[1];
-    // frames that some row of this CTA can see (the end distances stand for all beyond them); a
-    // wrapped ring keeps its frames out of order, and all of its slots are read
-    int f_lo = 0, f_hi = nframes - 1;
-    if (!wrapped) {
-        const int ta = start + dF.div(q_first), tb = start + dF.div(min(q_first + 2 * kBM, n_q) - 1);
-        if (dhi < dmax) f_lo = max(f_lo, ta - dhi);
-        if (dlo > -dmax) f_hi = min(f_hi, tb - dlo);
-    }
-    if (dlo > dhi) f_hi = f_lo - 1;
+    int f_lo, f_hi;  // frames that some row of this CTA can see
+    ring.visible(start + dF.div(q_first), start + dF.div(min(q_first + 2 * kBM, n_q) - 1), dlo, dhi, dmax, f_lo, f_hi);
     const int nkv_all = f_hi >= f_lo ? ((f_hi - f_lo + 1) * nF + kBN - 1) / kBN : 0;
     const int per_split = (nkv_all + p.splits - 1) / p.splits;
     const int jend = (f_hi + 1) * nF;                          // end of the visible keys
@@ -451,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 t.init((of_v ? p.cache.v : p.cache.k) + sh * p.cache.cap * p.cache.F * D, of_v ? v_scales : k_scales,
                        sbase + C::OFF_STAGE + (of_v ? CacheTile<D>::STAGE_BYTES : 0), pw, lane);
                 const int ref = refs[of_v];
-                const uint32_t ring = sbase + (of_v ? C::OFF_V : C::OFF_K);
+                const uint32_t slots = sbase + (of_v ? C::OFF_V : C::OFF_K);
                 auto fetch = [&](int j) {
                     t.fetch_scales(jbeg + j * kBN, jend, dF, nF, p.cache);
                     t.fetch(jbeg + j * kBN, jend, dF, nF, p.cache, p.status);
@@ -461,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 for (int j = 0; j < steps; ++j) {
                     cp_async_wait<0>();
                     if (!(ok = wait_empty(of_v, j))) break;
-                    const uint32_t dst = ring + (j % C::KST) * C::TILE_BYTES;
+                    const uint32_t dst = slots + (j % C::KST) * C::TILE_BYTES;
                     if (t.all_ref(ref))
                         t.template expand<false>(dst, ref);
                     else
@@ -589,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         const uint32_t sfull = bar(C::B_SFULL + qt);
         const int qi = q_first + qt * kBM + row;
         const int tq = start + dF.div(min(qi, n_q - 1));
-        auto bias_of = [&](int f) { return tab[clamp_dist(tq - frame_time(f), dmax) + dmax]; };
+        auto bias_of = [&](int f) { return tab[clamp_dist(tq - ring.time(f), dmax) + dmax]; };
         float m_run = -INFINITY, l_run = 0.f;  // in units of log2
         bool ok = true;
         float sl2 = p.scale_log2;
@@ -820,14 +794,13 @@ __global__ void __launch_bounds__(256) skiparse_frames_join_kernel(const FramesF
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     constexpr int PER = D / 32;
     float acc[PER] = {}, total = 0.f;
-    if (m != -INFINITY) {
-        for (int s = 0; s < p.splits; ++s) {
-            const float w = ptx::ex2_approx(l[s] - m);
-            total += w;
-            const float* o = p.part_o + (row * p.splits + s) * D + lane * PER;
+    m = m == -INFINITY ? 0.f : m;  // no key seen, or NaNs alone, which have to stay
+    for (int s = 0; s < p.splits; ++s) {
+        const float w = ptx::ex2_approx(l[s] - m);
+        total += w;
+        const float* o = p.part_o + (row * p.splits + s) * D + lane * PER;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
-        }
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
@@ -836,11 +809,14 @@ __global__ void __launch_bounds__(256) skiparse_frames_join_kernel(const FramesF
     if (lane == 0 && p.lse) p.lse[row] = total == 0.f ? -INFINITY : (m + ptx::lg2_approx(total)) * 0.6931471805599453f;
 }
 
-int max_class_tokens(const Geometry& g) {
-    int n = 0;
-    for (int ci = 0; ci < g.Ph; ++ci)
-        for (int cj = 0; cj < g.Pw; ++cj) n = g.Rc[ci] * g.Sc[cj] > n ? g.Rc[ci] * g.Sc[cj] : n;
-    return n;
+int launch_frames_join(const FramesFwdParams& p, int d, cudaStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>((p.nrows + 7) / 8);
+    switch (d) {
+        case 32: skiparse_frames_join_kernel<32><<<blocks, 256, 0, stream>>>(p); break;
+        case 64: skiparse_frames_join_kernel<64><<<blocks, 256, 0, stream>>>(p); break;
+        default: skiparse_frames_join_kernel<128><<<blocks, 256, 0, stream>>>(p); break;
+    }
+    return static_cast<int>(cudaGetLastError());
 }
 
 template <int D, bool CACHE>
@@ -869,8 +845,7 @@ int launch_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
     skiparse_attn_frames_kernel<D, CACHE><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return static_cast<int>(e);
-    skiparse_frames_join_kernel<D><<<static_cast<unsigned>((p.nrows + 7) / 8), 256, 0, stream>>>(p);
-    return static_cast<int>(cudaGetLastError());
+    return launch_frames_join(p, D, stream);
 }
 
 template <int D>
@@ -884,6 +859,7 @@ int launch_kind(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream
 // each part keeps at least four key tiles. The cache's capacity stands for its length, which
 // only the device knows.
 int cached_splits(const Geometry& g, int cap) {
+    if (cached_small(g)) return cached_small_splits(g, cap);
     const long long nF = max_class_tokens(g);
     const long long ctas = (g.T * nF + 2 * kBM - 1) / (2 * kBM) * g.heads * g.B * g.Ph * g.Pw;
     const long long tiles = (cap * nF + kBN - 1) / kBN;
@@ -894,6 +870,10 @@ int cached_splits(const Geometry& g, int cap) {
 
 int launch_frames_fwd(const FramesFwdParams& p, const Geometry& g, void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p.cache.k && cached_small(g)) {
+        const int e = launch_cached_small(p, g, stream);
+        return e || p.splits == 1 ? e : launch_frames_join(p, g.d, st);
+    }
     switch (g.d) {
         case 32: return launch_kind<32>(p, g, st);
         case 64: return launch_kind<64>(p, g, st);

@@ -51,15 +51,6 @@ size_t map_bytes(int max_distance) { return (2 * static_cast<size_t>(max_distanc
 
 double log2e_over_sqrt(int d) { return 1.4426950408889634 / std::sqrt(static_cast<double>(d)); }
 
-int max_class(const Geometry& g) {  // tokens of one frame in the largest class
-    int r = 0, s = 0;
-    for (int c = 0; c < skiparse::kMaxAxisClasses; ++c) {
-        r = g.Rc[c] > r ? g.Rc[c] : r;
-        s = g.Sc[c] > s ? g.Sc[c] : s;
-    }
-    return r * s;
-}
-
 // ------------------------------------------------------------------------ biased attention
 
 int relbias_fwd(int dims, const void* q, const void* k, const void* v, const void* table, const int* buckets,
@@ -111,7 +102,7 @@ BwdSpace bwd_space(const Geometry& g, int max_distance) {
     BwdSpace w;
     w.Dn = max_distance < g.T - 1 ? max_distance : g.T - 1;
     w.ND = 2 * w.Dn + 1;
-    const long long n = static_cast<long long>(g.T) * max_class(g);
+    const long long n = static_cast<long long>(g.T) * skiparse::max_class_tokens(g);
     w.tiles = static_cast<int>((n + 127) / 128);
     const size_t rows = static_cast<size_t>(g.B) * g.T * g.H * g.W * g.heads;
     w.lse2 = pad256(rows * 4);
@@ -244,7 +235,7 @@ int cache_append(int dims, const void* k, const void* v, const int* start, void*
     if (!(p.status = api::status_word())) return SKIPARSE_ERR_CUDA;
     skiparse::fill_frame_geom(p.g, g);
     p.cache = cache_view(g, k_cache, v_cache, k_scale, v_scale, start, capacity);
-    p.nblk = (max_class(g) + skiparse::kCacheBlock - 1) / skiparse::kCacheBlock;
+    p.nblk = (skiparse::max_class_tokens(g) + skiparse::kCacheBlock - 1) / skiparse::kCacheBlock;
     p.nrows = api::debug_bound(rows);
     const int e = skiparse::launch_cache_append(p, g, d, stream);
     return e == 0 ? SKIPARSE_OK : api::cuda_fail(e);

@@ -109,9 +109,23 @@ struct AppendParams {
 int launch_frames_fwd(const FramesFwdParams& p, const Geometry& g, void* stream);
 int launch_frames_bwd(const FramesBwdParams& p, const Geometry& g, void* stream);
 int launch_cache_append(const AppendParams& p, const Geometry& g, int d, void* stream);
+// Attention of few queries over the cache: whether a call's classes are small enough for it, its
+// splits, and its launch (without the joining of the splits).
+bool cached_small(const Geometry& g);
+int cached_small_splits(const Geometry& g, int cap);
+int launch_cached_small(const FramesFwdParams& p, const Geometry& g, void* stream);
 // Key splits that launch_frames_fwd should be given for a cache call of these sizes (1: no
 // workspace is needed).
 int cached_splits(const Geometry& g, int cap);
+
+inline int max_class_tokens(const Geometry& g) {  // tokens of one frame in the largest class
+    int r = 0, s = 0;
+    for (int c = 0; c < kMaxAxisClasses; ++c) {
+        r = g.Rc[c] > r ? g.Rc[c] : r;
+        s = g.Sc[c] > s ? g.Sc[c] : s;
+    }
+    return r * s;
+}
 
 inline void fill_frame_geom(FrameGeom& f, const Geometry& g) {
     f.T = g.T; f.H = g.H; f.W = g.W; f.heads = g.heads; f.Ph = g.Ph; f.Pw = g.Pw; f.mode = g.mode;
