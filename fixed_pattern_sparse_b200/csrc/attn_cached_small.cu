@@ -96,20 +96,18 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
     const int split = blockIdx.x / row_tiles, tile = blockIdx.x % row_tiles;
     const int head = blockIdx.y;
     const int seq = blockIdx.z;
-    const int q2 = p.g.Ph * p.g.Pw;
-    const int b = seq / q2, c2 = seq % q2, ci = c2 / p.g.Pw, cj = c2 % p.g.Pw;
-    const int Rc = p.g.Rc[ci], Sc = p.g.Sc[cj], nF = Rc * Sc;
+    ClassView cls;
+    cls.init(p.g, seq);
+    const int nF = cls.nF;
+    const FastDiv dF = cls.dF;
     const int n_q = p.g.T * nF;
     const int q_first = tile * C::ROWS;
     if (q_first >= n_q) return;
-    const int start = p.cache.start[b];
+    const int start = p.cache.start[cls.b];
     if (start < 0 || start > kMaxStart) return;
     FrameRing ring;
     ring.init(start + p.g.T, p.cache.cap);
-    FastDiv dF;
-    dF.init(nF);
-    RowMap rows;
-    rows.init(p.g.T, p.g.H, p.g.W, p.g.heads, p.g.Ph, p.g.Pw, p.g.mode, ci, cj, Rc, Sc, b, head);
+    const RowMap rows = cls.rows(p.g, head);
 
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);

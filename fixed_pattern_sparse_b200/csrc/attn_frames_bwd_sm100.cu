@@ -100,16 +100,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
     const int tile = KV ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
     const int head = blockIdx.y;
     const int seq = blockIdx.z;
-    const int q2 = p.g.Ph * p.g.Pw;
-    const int b = seq / q2, c = seq % q2, ci = c / p.g.Pw, cj = c % p.g.Pw;
-    const int Rc = p.g.Rc[ci], Sc = p.g.Sc[cj], nF = Rc * Sc;
+    ClassView cls;
+    cls.init(p.g, seq);
+    const int nF = cls.nF;
+    const FastDiv dF = cls.dF;
     const int n_c = p.g.T * nF;
     const int first = tile * kTileRows;
     if (first >= n_c) return;  // uniform over the CTA, before any shared state
-    RowMap rows;
-    rows.init(p.g.T, p.g.H, p.g.W, p.g.heads, p.g.Ph, p.g.Pw, p.g.mode, ci, cj, Rc, Sc, b, head);
-    FastDiv dF;
-    dF.init(nF);
+    const RowMap rows = cls.rows(p.g, head);
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_u32(smem_raw);

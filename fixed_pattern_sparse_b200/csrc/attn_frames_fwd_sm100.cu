@@ -277,15 +277,16 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int pair = npairs - 1 - blockIdx.x / p.splits;
     const int head = blockIdx.y;
     const int seq = blockIdx.z;
-    const int q2 = p.g.Ph * p.g.Pw;
-    const int b = seq / q2, c = seq % q2, ci = c / p.g.Pw, cj = c % p.g.Pw;
-    const int Rc = p.g.Rc[ci], Sc = p.g.Sc[cj], nF = Rc * Sc;
+    ClassView cls;
+    cls.init(p.g, seq);
+    const int nF = cls.nF;
+    const FastDiv dF = cls.dF;
     const int n_q = p.g.T * nF;
     const int q_first = pair * 2 * kBM;
     if (q_first >= n_q) return;  // uniform over the CTA, before any shared state
     int start = 0;
     if (CACHE) {
-        start = p.cache.start[b];
+        start = p.cache.start[cls.b];
         if (start < 0 || start > kMaxStart) return;  // a sequence without new frames
     }
     FrameRing ring;
@@ -313,10 +314,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int lane = threadIdx.x & 31;
     const uint64_t lim = p.wait_limit_ns;
     const int dmax = p.bias.D;
-    RowMap rows;
-    rows.init(p.g.T, p.g.H, p.g.W, p.g.heads, p.g.Ph, p.g.Pw, p.g.mode, ci, cj, Rc, Sc, b, head);
-    FastDiv dF;
-    dF.init(nF);
+    const RowMap rows = cls.rows(p.g, head);
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(C::B_Q), 64);

@@ -37,15 +37,22 @@ __global__ void __launch_bounds__(kThreads) skiparse_cache_append_kernel(const A
     const int t = blockIdx.x / p.g.heads / p.nblk;
     const int seq = blockIdx.y;
     const bool is_v = blockIdx.z;
-    const int q2 = p.g.Ph * p.g.Pw;
-    const int b = seq / q2, c = seq % q2, ci = c / p.g.Pw, cj = c % p.g.Pw;
-    const int Rc = p.g.Rc[ci], Sc = p.g.Sc[cj], nF = Rc * Sc;
+    ClassView cls;
+    cls.init(p.g, seq);
+    const int nF = cls.nF;
     const int first = blk * kCacheBlock;
     if (first >= nF) return;
-    const int start = p.cache.start[b];
+    const int start = p.cache.start[cls.b];
     if (start < 0 || start > kMaxStart) return;
     const int slot = (start + t) % p.cache.cap;
     const uint16_t* src = is_v ? p.v : p.k;
+    // rows of the block's tokens, each computed once
+    __shared__ int row_of[kCacheBlock];
+    if (threadIdx.x < kCacheBlock && first + threadIdx.x < nF) {
+        const RowMap rows = cls.rows(p.g, head);
+        row_of[threadIdx.x] = static_cast<int>(load_row(rows(t * nF + first + threadIdx.x), p.nrows, p.status));
+    }
+    __syncthreads();
 
     uint4 x[PER];
     uint32_t top = 0;  // bits of the largest magnitude, two at a time
@@ -55,11 +62,7 @@ __global__ void __launch_bounds__(kThreads) skiparse_cache_append_kernel(const A
         const int tok = first + ch / CPR;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (tok < nF) {
-            const int r = tok / Sc, s = tok - r * Sc;
-            const int h = axis_coord(r, ci, p.g.Ph, p.g.mode), w = axis_coord(s, cj, p.g.Pw, p.g.mode);
-            const long long row =
-                (((static_cast<long long>(b) * p.g.T + t) * p.g.H + h) * p.g.W + w) * p.g.heads + head;
-            const uint4* at = reinterpret_cast<const uint4*>(src + load_row(row, p.nrows, p.status) * D) + ch % CPR;
+            const uint4* at = reinterpret_cast<const uint4*>(src + static_cast<size_t>(row_of[ch / CPR]) * D) + ch % CPR;
             asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
                          : "l"(at));

@@ -6,7 +6,6 @@
 
 #include <cstdint>
 
-#include "attn_common.cuh"
 #include "frames_internal.cuh"
 
 namespace skiparse {

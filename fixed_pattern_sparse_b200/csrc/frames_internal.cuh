@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "attn_common.cuh"
 #include "skiparse_internal.cuh"
 
 namespace skiparse {
@@ -22,10 +23,13 @@ struct FrameBias {
     int D, NB;
 };
 
-// Where the dimensions of a call lie; filled from Geometry.
+// The dimensions of a call, filled from Geometry, and the divisions that the kernels need: by the
+// rows, columns and tokens per frame of each class and by the class counts. (Their constants take a
+// thread a 64-bit division each; in small calls those were a good part of the kernel's time.)
 struct FrameGeom {
     int T, H, W, heads, Ph, Pw, mode;
     int Rc[kMaxAxisClasses], Sc[kMaxAxisClasses];
+    FastDiv dR[kMaxAxisClasses], dS[kMaxAxisClasses], dF[kMaxAxisClasses], dPh, dPw;
 };
 
 // The e4m3 frame cache of one layer: codes (B*classes, heads, cap, F, d), F the padded tokens
@@ -132,7 +136,36 @@ inline void fill_frame_geom(FrameGeom& f, const Geometry& g) {
     for (int c = 0; c < kMaxAxisClasses; ++c) {
         f.Rc[c] = g.Rc[c];
         f.Sc[c] = g.Sc[c];
+        f.dR[c].init(g.Rc[c]);
+        f.dS[c].init(g.Sc[c]);
+        if (c < g.Ph * g.Pw) f.dF[c].init(g.Rc[c / g.Pw] * g.Sc[c % g.Pw]);
     }
+    f.dPh.init(g.Ph);
+    f.dPw.init(g.Pw);
 }
+
+// One (batch, class, head) of a call: its sizes and row map.
+struct ClassView {
+    int b, c, ci, cj, Rc, Sc, nF;  // nF: tokens per frame
+    FastDiv dF;
+    __device__ __forceinline__ void init(const FrameGeom& g, int seq) {
+        const int q2 = g.Ph * g.Pw;
+        b = seq / q2;
+        c = seq - b * q2;
+        ci = c / g.Pw;
+        cj = c - ci * g.Pw;
+        Rc = g.Rc[ci];
+        Sc = g.Sc[cj];
+        nF = Rc * Sc;
+        dF = g.dF[c];
+    }
+    __device__ __forceinline__ RowMap rows(const FrameGeom& g, int head) const {
+        RowMap r;
+        r.T = g.T; r.H = g.H; r.W = g.W; r.heads = g.heads; r.Ph = g.Ph; r.Pw = g.Pw; r.mode = g.mode;
+        r.ci = ci; r.cj = cj; r.Rc = Rc; r.Sc = Sc; r.b = b; r.head = head;
+        r.dSc = g.dS[cj]; r.dRc = g.dR[ci]; r.dPh = g.dPh; r.dPw = g.dPw;
+        return r;
+    }
+};
 
 }  // namespace skiparse

@@ -10,7 +10,7 @@ allocates (outputs, workspaces) belongs to the stream it works on.
 
 from __future__ import annotations
 
-import contextlib
+import functools
 import math
 from typing import NamedTuple
 
@@ -83,7 +83,16 @@ def _entry(name: str, dims: int):
     return getattr(lib(), name.replace("@", "1d" if dims == 1 else "2d"))
 
 
-def _need(name: str, t, dtype, shape=None, device=None) -> None:
+@functools.lru_cache(maxsize=256)
+def _size_of(name: str, *args) -> int:
+    """A size the library computes from sizes alone; name is the entry point's."""
+    return getattr(lib(), name)(*args)
+
+
+def _need(name: str, t, dtype, shape=None, device: int | None = None) -> None:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (device is None or t.get_device() == device)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if t.dtype != dtype:
@@ -92,88 +101,95 @@ def _need(name: str, t, dtype, shape=None, device=None) -> None:
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-def _tokens(name: str, t, like=None) -> None:
-    _need(name, t, torch.bfloat16, None if like is None else like.shape, None if like is None else like.device)
+def _tokens(name: str, t):
+    """Checks a (B,T,H,W,heads,d) tensor; returns its shape and device index."""
+    _need(name, t, torch.bfloat16)
     if t.dim() != 6:
         raise ValueError(f"{name} must be (B,T,H,W,heads,d)")
+    return t.shape, t.get_device()
 
 
-def _bias(table, buckets, heads: int, device):
+def _bias(table, buckets, heads: int, device: int):
     """Pointers and sizes of the bias arguments."""
     _need("table", table, torch.bfloat16, None, device)
     _need("buckets", buckets, torch.int32, None, device)
     if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] != heads:
         raise ValueError(f"table must be (num_buckets, {heads})")
-    if buckets.dim() != 1 or buckets.numel() % 2 == 0 or buckets.numel() > 511:
+    n = buckets.numel()
+    if buckets.dim() != 1 or n % 2 == 0 or n > 511:
         raise ValueError("buckets must hold 2*max_distance+1 entries, max_distance <= 255")
-    return table.data_ptr(), buckets.data_ptr(), table.shape[0], buckets.numel() // 2
+    return table.data_ptr(), buckets.data_ptr(), table.shape[0], n // 2
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The stream to work on, current while the call allocates and launches."""
+def _on(device: int, stream, call):
+    """Runs call(stream pointer) with the tensors' device and the stream to work on current, so that
+    what it allocates belongs to that stream."""
+    if stream is None and device == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
     with torch.cuda.device(device):
-        s = torch.cuda.current_stream(device) if stream is None else stream
         if stream is None:
-            yield s.cuda_stream
-        else:
-            with torch.cuda.stream(s):
-                yield s.cuda_stream
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _relbias_fwd(dims, q, k, v, table, buckets, P, mode, out, lse, out_lo, stream):
-    _tokens("q", q)
-    _tokens("k", k, q)
-    _tokens("v", v, q)
-    B, T, H, W, heads, d = q.shape
-    bias = _bias(table, buckets, heads, q.device)
+    shape, dev = _tokens("q", q)
+    bf16 = torch.bfloat16
+    _need("k", k, bf16, shape, dev)
+    _need("v", v, bf16, shape, dev)
+    bias = _bias(table, buckets, shape[4], dev)
+    if out is not None:
+        _need("out", out, bf16, shape, dev)
+    if out_lo is not None:
+        _need("out_lo", out_lo, bf16, shape, dev)
+    if lse is not None:
+        _need("lse", lse, torch.float32, shape[:5], dev)
     name = "skiparse@_attn_relbias_fwd"
-    with _on(q.device, stream) as st:
-        out = torch.empty_like(q) if out is None else out
-        _tokens("out", out, q)
-        if out_lo is not None:
-            _tokens("out_lo", out_lo, q)
-        if lse is None:
-            lse = torch.empty(q.shape[:5], dtype=torch.float32, device=q.device)
-        _need("lse", lse, torch.float32, q.shape[:5], q.device)
-        check(_entry(name, dims)(q.data_ptr(), k.data_ptr(), v.data_ptr(), *bias, out.data_ptr(),
-                                 None if out_lo is None else out_lo.data_ptr(), lse.data_ptr(), B, T, H, W, heads, d, P, mode, st),
-              name.replace("@", f"{dims}d"))
-    return out, lse
+
+    def call(st):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty(shape[:5], dtype=torch.float32, device=q.device) if lse is None else lse
+        check(_entry(name, dims)(q.data_ptr(), k.data_ptr(), v.data_ptr(), *bias, o.data_ptr(),
+                                 None if out_lo is None else out_lo.data_ptr(), l.data_ptr(), *shape, P, mode, st), name)
+        return o, l
+
+    return _on(dev, stream, call)
 
 
 def _relbias_bwd(dims, q, k, v, out, dout, lse, table, buckets, P, mode, dq, dk, dv, dtable, out_lo, workspace,
                  stream):
-    _tokens("q", q)
+    shape, dev = _tokens("q", q)
+    bf16 = torch.bfloat16
     for what, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
-        _tokens(what, t, q)
-    if out_lo is not None:
-        _tokens("out_lo", out_lo, q)
-    B, T, H, W, heads, d = q.shape
-    _need("lse", lse, torch.float32, q.shape[:5], q.device)
-    bias = _bias(table, buckets, heads, q.device)
+        _need(what, t, bf16, shape, dev)
+    _need("lse", lse, torch.float32, shape[:5], dev)
+    bias = _bias(table, buckets, shape[4], dev)
+    for what, t in (("out_lo", out_lo), ("dq", dq), ("dk", dk), ("dv", dv)):
+        if t is not None:
+            _need(what, t, bf16, shape, dev)
+    if dtable is not None:
+        _need("dtable", dtable, bf16, table.shape, dev)
+    if workspace is not None:
+        _need("workspace", workspace, torch.uint8, None, dev)
     name = "skiparse@_attn_relbias_bwd"
-    need = _entry(name + "_workspace_bytes", dims)(B, T, H, W, heads, d, P, bias[3])
+    need = _size_of(f"skiparse{dims}d_attn_relbias_bwd_workspace_bytes", *shape, P, bias[3])
     if need < 0:
         raise ValueError("invalid shape or P")
-    with _on(q.device, stream) as st:
-        dq, dk, dv = (torch.empty_like(q) if g is None else g for g in (dq, dk, dv))
-        dtable = torch.empty_like(table) if dtable is None else dtable
-        for what, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-            _tokens(what, t, q)
-        _need("dtable", dtable, torch.bfloat16, table.shape, q.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _need("workspace", workspace, torch.uint8, None, q.device)
+
+    def call(st):
+        grads = [torch.empty_like(q) if g is None else g for g in (dq, dk, dv)]
+        grads.append(torch.empty_like(table) if dtable is None else dtable)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
         check(_entry(name, dims)(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 None if out_lo is None else out_lo.data_ptr(), dout.data_ptr(), lse.data_ptr(), *bias, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                 dtable.data_ptr(), workspace.data_ptr(), workspace.numel(), B, T, H, W, heads, d, P,
-                                 mode, st), name.replace("@", f"{dims}d"))
-    return dq, dk, dv, dtable
+                                 None if out_lo is None else out_lo.data_ptr(), dout.data_ptr(), lse.data_ptr(), *bias,
+                                 *(g.data_ptr() for g in grads), ws.data_ptr(), ws.numel(), *shape, P, mode, st), name)
+        return tuple(grads)
+
+    return _on(dev, stream, call)
 
 
 def skiparse2d_attn_relbias_fwd(q, k, v, table, buckets, P: int, mode: int, out=None, lse=None, out_lo=None,
@@ -230,61 +246,75 @@ class SkiparseRelBiasAttention(torch.autograd.Function):
         return (*grads, None, None, None, None)
 
 
-def _cache_shapes(dims, cache, B, H, W, heads, d, P, device):
+def _cache_shapes(dims, cache, shape, P, device):
     """Checks a cache against a call's sizes; returns its capacity."""
-    F = _entry("skiparse@_cache_frame_tokens", dims)(H, W, P)
+    B, _, H, W, heads, d = shape
+    if dims not in (1, 2):
+        raise ValueError("dims must be 1 (Skiparse-1D) or 2 (Skiparse-2D)")
+    F = _size_of(f"skiparse{dims}d_cache_frame_tokens", H, W, P)
     if F < 0:
         raise ValueError("invalid shape or P")
-    if not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 5:
+    k, v, k_scale, v_scale = cache
+    if not isinstance(k, torch.Tensor) or k.dim() != 5:
         raise ValueError("cache.k must be (B*P*P, heads, capacity, F, d)")
-    rows = (B * P * P, heads, cache.capacity, F)
-    for what, t in (("cache.k", cache.k), ("cache.v", cache.v)):
-        _need(what, t, torch.float8_e4m3fn, rows + (d,), device)
-    for what, t in (("cache.k_scale", cache.k_scale), ("cache.v_scale", cache.v_scale)):
-        _need(what, t, torch.float8_e8m0fnu, rows[:3] + (-(-F // BLOCK),), device)
-    return cache.capacity
+    capacity = k.shape[2]
+    rows = (B * P * P, heads, capacity, F)
+    _need("cache.k", k, torch.float8_e4m3fn, rows + (d,), device)
+    _need("cache.v", v, torch.float8_e4m3fn, rows + (d,), device)
+    blocks = rows[:3] + (-(-F // BLOCK),)
+    _need("cache.k_scale", k_scale, torch.float8_e8m0fnu, blocks, device)
+    _need("cache.v_scale", v_scale, torch.float8_e8m0fnu, blocks, device)
+    return capacity
 
 
 def _cache_append(dims, k, v, start, cache, P, mode, stream):
-    _tokens("k", k)
-    _tokens("v", v, k)
-    B, T, H, W, heads, d = k.shape
-    _need("start", start, torch.int32, (B,), k.device)
-    capacity = _cache_shapes(dims, cache, B, H, W, heads, d, P, k.device)
+    shape, dev = _tokens("k", k)
+    _need("v", v, torch.bfloat16, shape, dev)
+    _need("start", start, torch.int32, shape[:1], dev)
+    if cache is None:
+        raise ValueError("cache must be a FrameCache")
+    capacity = _cache_shapes(dims, cache, shape, P, dev)
     name = "skiparse@_cache_append"
-    with _on(k.device, stream) as st:
+
+    def call(st):
         check(_entry(name, dims)(k.data_ptr(), v.data_ptr(), start.data_ptr(), *(t.data_ptr() for t in cache),
-                                 B, T, H, W, heads, d, P, mode, capacity, st), name.replace("@", f"{dims}d"))
-    return cache
+                                 *shape, P, mode, capacity, st), name)
+        return cache
+
+    return _on(dev, stream, call)
 
 
 def _attn_cached(dims, q, cache, start, P, mode, table, buckets, out, lse, workspace, stream):
-    _tokens("q", q)
-    B, T, H, W, heads, d = q.shape
-    _need("start", start, torch.int32, (B,), q.device)
-    capacity = _cache_shapes(dims, cache, B, H, W, heads, d, P, q.device)
+    shape, dev = _tokens("q", q)
+    _need("start", start, torch.int32, shape[:1], dev)
+    if cache is None:
+        raise ValueError("cache must be a FrameCache")
+    capacity = _cache_shapes(dims, cache, shape, P, dev)
     if (table is None) != (buckets is None):
         raise ValueError("table and buckets belong together")
-    bias = (None, None, 0, 0) if table is None else _bias(table, buckets, heads, q.device)
+    bias = (None, None, 0, 0) if table is None else _bias(table, buckets, shape[4], dev)
+    if out is not None:
+        _need("out", out, torch.bfloat16, shape, dev)
+    if lse is not None:
+        _need("lse", lse, torch.float32, shape[:5], dev)
+    if workspace is not None:
+        _need("workspace", workspace, torch.uint8, None, dev)
     name = "skiparse@_attn_cached"
-    need = _entry(name + "_workspace_bytes", dims)(B, T, H, W, heads, d, P, capacity)
+    need = _size_of(f"skiparse{dims}d_attn_cached_workspace_bytes", *shape, P, capacity)
     if need < 0:
         raise ValueError("invalid shape, P or capacity")
-    with _on(q.device, stream) as st:
-        out = torch.empty_like(q) if out is None else out
-        _tokens("out", out, q)
-        if lse is not None:
-            _need("lse", lse, torch.float32, q.shape[:5], q.device)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if workspace is not None:
-            _need("workspace", workspace, torch.uint8, None, q.device)
-        check(_entry(name, dims)(q.data_ptr(), *(t.data_ptr() for t in cache), start.data_ptr(), *bias,
-                                 out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(),
-                                 0 if workspace is None else workspace.numel(), B, T, H, W, heads, d, P, mode,
-                                 capacity, st), name.replace("@", f"{dims}d"))
-    return out
+
+    def call(st):
+        o = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        check(_entry(name, dims)(q.data_ptr(), *(t.data_ptr() for t in cache), start.data_ptr(), *bias, o.data_ptr(),
+                                 None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+                                 0 if ws is None else ws.numel(), *shape, P, mode, capacity, st), name)
+        return o
+
+    return _on(dev, stream, call)
 
 
 def skiparse2d_cache_append(k, v, start, cache: FrameCache, P: int, mode: int, stream=None) -> FrameCache:
