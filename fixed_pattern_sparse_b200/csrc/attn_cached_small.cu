@@ -22,8 +22,8 @@
 // lane and step at d = 128, 4 clocks each) keep below the 180 clocks in which an SM's share
 // of HBM delivers its 4 KB.
 // Key groups are dealt to the warps of a CTA and, over long caches, to `splits` CTAs; warps join
-// through shared memory, CTAs through the join kernel of attn_frames_fwd_sm100.cu. Queries beyond a
-// CTA's 8, 16 or 32 go to further CTAs that re-read the keys, from L2 when they run together.
+// through shared memory, CTAs through the join kernel of attn_frames_fwd_sm100.cu. A CTA has
+// 8, 16 or 32 queries.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,7 +37,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kKeys = 16;      // keys of a warp step
 constexpr int kStages = 4;
-constexpr int kMaxRows = 64;   // queries per class up to which this kernel is used
+constexpr int kMaxRows = 32;   // queries per class up to which this kernel is used (measured, 57,000 keys,
+                               // d = 128: 30 queries 0.49 ms against the tcgen05 kernel's 0.80, 64: 0.89, 0.52)
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D, int NQ>  // NQ: tiles of 8 queries of a CTA
@@ -457,12 +458,13 @@ int launch_small(const FramesFwdParams& p, const Geometry& g, cudaStream_t strea
 
 bool cached_small(const Geometry& g) { return static_cast<long long>(g.T) * max_class_tokens(g) <= kMaxRows; }
 
-// At least 512 keys a CTA, and no more CTAs than some four waves of three per SM.
+// One wave of CTAs, of at least 512 keys each (measured: 2 to 3 times as many CTAs cost up to a fifth
+// in small calls and change nothing in large ones).
 int cached_small_splits(const Geometry& g, int cap) {
     const long long n = static_cast<long long>(g.T) * max_class_tokens(g), rows = 8 * query_tiles(n);
     const long long keys = static_cast<long long>(cap) * max_class_tokens(g);
     const long long ctas = (n + rows - 1) / rows * g.heads * g.B * g.Ph * g.Pw;
-    long long s = 4LL * 3 * 148 / ctas;
+    long long s = 3 * 148 / ctas;
     if (s > keys / 512) s = keys / 512;
     return static_cast<int>(s < 1 ? 1 : s);
 }

@@ -27,6 +27,9 @@
 //   * Few query tiles over a long cache leave SMs idle: the key range is then cut into `splits`
 //     parts, each CTA writes its normalised partial output and log-sum-exp in fp32, and
 //     a second kernel joins them.
+//   * Calls of few query tiles: a CTA may own 128 queries instead, its two softmax groups taking
+//     every other key tile each (an own O in TMEM each, joined at the end), which halves the
+//     length of a CTA and doubles their number.
 // Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB, staging 32 KB.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -100,7 +103,7 @@ struct CacheTile {
     static constexpr int NG = kBN / RPI;          // row groups of a tile
     static constexpr int PER = (NG + 2) / 3;      // row groups of a warp
     static constexpr int STAGE_BYTES = NG * 512;  // a tile of codes
-    uint32_t byte[PER < 3 ? 3 : PER];             // scale bytes
+    uint32_t byte[PER < 3 ? 3 : PER];             // scale bytes, then factors
     int at0;                                      // of the tile whose bytes these are: its first token's
     bool inside;                                  // place in its frame, and whether it lies in one
     const uint8_t* codes;                         // of this (subsequence, head)
@@ -116,73 +119,65 @@ struct CacheTile {
         lane = lane_;
         stage = stage_base + pw * 512 + lane * 16;
     }
-    // Starts the copies of the keys j0..j0+127 of the class, those from jend on repeating the last.
-    __device__ __forceinline__ void fetch(int j0, int jend, const FastDiv& dF, int nF, const CacheView& cv, int* status) const {
+    // Starts the copies of the keys j0..j0+127 of the class, those from jend on repeating the last, and
+    // loads their scale bytes: of a tile inside one frame the three that it can meet, else one a row.
+    __device__ __forceinline__ void fetch(int j0, int jend, const FastDiv& dF, int nF, const CacheView& cv, int* status) {
         const int c = lane % CPR, rsub = lane / CPR;
-        const int slot0 = dF.div(j0), at0 = j0 - slot0 * nF;
+        const int slot0 = dF.div(j0);
+        at0 = j0 - slot0 * nF;
+        inside = at0 + kBN <= nF && j0 + kBN <= jend;
         const long long rows = static_cast<long long>(cv.cap) * cv.F;
-        if (at0 + kBN <= nF && j0 + kBN <= jend) {  // inside one frame: constant strides
-            const long long row0 = load_row(static_cast<long long>(slot0) * cv.F + at0 + pw * RPI + rsub, rows, status);
+        const int gap = cv.F - nF;  // unused places of a slot
+        if (inside) {
+            const long long row0 = load_row(j0 + static_cast<long long>(slot0) * gap + pw * RPI + rsub, rows, status);
             const uint8_t* src = codes + row0 * D + c * 16;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (mine(i, pw)) cp_async_16(stage + i * 3 * 512, src + i * 3 * RPI * D);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (mine(i, pw)) {
-                    const int j = min(j0 + (pw + 3 * i) * RPI + rsub, jend - 1);
-                    const int slot = dF.div(j), at = j - slot * nF;
-                    const long long row = load_row(static_cast<long long>(slot) * cv.F + at, rows, status);
-                    cp_async_16(stage + i * 3 * 512, codes + row * D + c * 16);
-                }
-        }
-        cp_async_commit();
-    }
-    // Loads the scale bytes of the same rows: of a tile inside one frame the three that it can meet.
-    __device__ __forceinline__ void fetch_scales(int j0, int jend, const FastDiv& dF, int nF, const CacheView& cv) {
-        const int slot0 = dF.div(j0);
-        at0 = j0 - slot0 * nF;
-        inside = at0 + kBN <= nF && j0 + kBN <= jend;
-        if (inside) {
             const uint8_t* sc = scales + static_cast<long long>(slot0) * cv.NBk;
             const int last = (at0 + kBN - 1) / kCacheBlock;
 #pragma unroll
             for (int i = 0; i < 3; ++i) byte[i] = __ldg(sc + min(at0 / kCacheBlock + i, last));
         } else {
-            const int rsub = lane / CPR;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (mine(i, pw)) {
                     const int j = min(j0 + (pw + 3 * i) * RPI + rsub, jend - 1);
-                    const int slot = dF.div(j), at = j - slot * nF;
-                    byte[i] = __ldg(scales + static_cast<long long>(slot) * cv.NBk + at / kCacheBlock);
+                    const int slot = dF.div(j);
+                    const long long row = load_row(j + static_cast<long long>(slot) * gap, rows, status);
+                    cp_async_16(stage + i * 3 * 512, codes + row * D + c * 16);
+                    byte[i] = __ldg(scales + slot * cv.NBk + (j - slot * nF) / kCacheBlock);
                 }
         }
+        cp_async_commit();
     }
-    // Whether every scale of the warp's rows is the reference; if not, byte[] is filled row by row.
+    // Whether every scale of the warp's rows is the reference; if not, byte[] becomes the factors
+    // 2^(scale - ref) row by row.
     __device__ __forceinline__ bool all_ref(int ref) {
         const uint32_t r = static_cast<uint32_t>(ref);
         if (inside) {
             const uint32_t b0 = byte[0], b1 = byte[1], b2 = byte[2];
             if (b0 == r && b1 == r && b2 == r) return true;
+            const uint32_t m0 = scale_f16x2(b0, ref), m1 = scale_f16x2(b1, ref), m2 = scale_f16x2(b2, ref);
             const int r0 = at0 % kCacheBlock + pw * RPI + lane / CPR;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int blk = (r0 + 3 * i * RPI) / kCacheBlock;
-                byte[i] = blk == 0 ? b0 : blk == 1 ? b1 : b2;
-            }
+            for (int i = 0; i < PER; ++i)
+                byte[i] = r0 + 3 * i * RPI < kCacheBlock ? m0 : r0 + 3 * i * RPI < 2 * kCacheBlock ? m1 : m2;
             return false;
         }
         bool one = true;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (mine(i, pw)) one = one && byte[i] == r;
-        return __all_sync(0xffffffffu, one);
+        if (__all_sync(0xffffffffu, one)) return true;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (mine(i, pw)) byte[i] = scale_f16x2(byte[i], ref);
+        return false;
     }
-    // Expands the staged tile into the swizzled f16 tile at dst, times 2^(scale - ref).
+    // Expands the staged tile into the swizzled f16 tile at dst, times byte[] if SCALED.
     template <bool SCALED>
-    __device__ __forceinline__ void expand(uint32_t dst, int ref) const {
+    __device__ __forceinline__ void expand(uint32_t dst) const {
         using C = TileGeom<D>;
         const int c = lane % CPR, rsub = lane / CPR;
         // A chunk gives two 16-byte stores; the lanes of a row's second box start with their second
@@ -194,7 +189,8 @@ struct CacheTile {
         const uint32_t odd[2] = {dst + tile_chunk<D>(r0 + 3 * RPI, 2 * c + flip) - 3 * RPI * C::SW,
                                  dst + tile_chunk<D>(r0 + 3 * RPI, 2 * c + 1 - flip) - 3 * RPI * C::SW};
         const uint32_t half_at[2] = {stage + 8 * flip, stage + 8 - 8 * flip};
-        // loads in batches, ahead of the conversions that use them
+        // loads in batches, ahead of the conversions that use them (all of them at once, to free the
+        // staging buffer for the next tile earlier, was slower: the registers do not suffice)
         constexpr int BATCH = 4;
 #pragma unroll
         for (int i0 = 0; i0 < PER; i0 += BATCH) {
@@ -210,20 +206,18 @@ struct CacheTile {
 #pragma unroll
             for (int i = i0; i < i0 + BATCH && i < PER; ++i)
                 if (mine(i, pw)) {
-                    uint32_t m = 0;
-                    if (SCALED) m = scale_f16x2(byte[i], ref);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const uint32_t* c = w[2 * (i - i0) + half];
+                        const uint32_t* x = w[2 * (i - i0) + half];
                         uint32_t y[4];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            y[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(c[e]));
-                            y[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(c[e] >> 16));
+                            y[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[e]));
+                            y[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[e] >> 16));
                         }
                         if (SCALED) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] = f16x2_mul(y[e], m);
+                            for (int e = 0; e < 4; ++e) y[e] = f16x2_mul(y[e], byte[i]);
                         }
                         const uint32_t at = ((i & 1) ? odd[half] : even[half]) + i * 3 * RPI * C::SW;
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
@@ -282,7 +276,8 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int nF = cls.nF;
     const FastDiv dF = cls.dF;
     const int n_q = p.g.T * nF;
-    const int q_first = pair * 2 * kBM;
+    const bool halves = p.halves;  // both tiles are the same 128 queries, each over half of the key tiles
+    const int q_first = pair * (halves ? kBM : 2 * kBM);
     if (q_first >= n_q) return;  // uniform over the CTA, before any shared state
     int start = 0;
     if (CACHE) {
@@ -360,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     dlo = range[0];
     dhi = range[1];
     int f_lo, f_hi;  // frames that some row of this CTA can see
-    ring.visible(start + dF.div(q_first), start + dF.div(min(q_first + 2 * kBM, n_q) - 1), dlo, dhi, dmax, f_lo, f_hi);
+    ring.visible(start + dF.div(q_first), start + dF.div(min(q_first + (halves ? kBM : 2 * kBM), n_q) - 1), dlo, dhi, dmax, f_lo, f_hi);
     const int nkv_all = f_hi >= f_lo ? ((f_hi - f_lo + 1) * nF + kBN - 1) / kBN : 0;
     const int per_split = (nkv_all + p.splits - 1) / p.splits;
     const int jend = (f_hi + 1) * nF;                          // end of the visible keys
@@ -414,7 +409,8 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             };
             if (nkv > 0 && pw < 2 && !of_v) {
                 load_tile<D>(sbase + C::OFF_Q, p.q, rows, q_first, n_q, pw, lane, p.nrows, p.status);
-                load_tile<D>(sbase + C::OFF_Q + C::TILE_BYTES, p.q, rows, q_first + kBM, n_q, pw, lane, p.nrows, p.status);
+                load_tile<D>(sbase + C::OFF_Q + C::TILE_BYTES, p.q, rows, halves ? q_first : q_first + kBM, n_q, pw,
+                             lane, p.nrows, p.status);
                 cp_async_arrive_noinc(bar(C::B_Q));
             }
             if constexpr (CACHE) {
@@ -424,26 +420,23 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                        sbase + C::OFF_STAGE + (of_v ? CacheTile<D>::STAGE_BYTES : 0), pw, lane);
                 const int ref = refs[of_v];
                 const uint32_t slots = sbase + (of_v ? C::OFF_V : C::OFF_K);
-                auto fetch = [&](int j) {
-                    t.fetch_scales(jbeg + j * kBN, jend, dF, nF, p.cache);
-                    t.fetch(jbeg + j * kBN, jend, dF, nF, p.cache, p.status);
-                };
                 const int steps = pw < 3 ? nkv : 0;
-                if (steps > 0) fetch(0);
+                if (steps > 0) t.fetch(jbeg, jend, dF, nF, p.cache, p.status);
                 for (int j = 0; j < steps; ++j) {
                     cp_async_wait<0>();
+                    const bool one = t.all_ref(ref);
                     if (!(ok = wait_empty(of_v, j))) break;
                     const uint32_t dst = slots + (j % C::KST) * C::TILE_BYTES;
-                    if (t.all_ref(ref))
-                        t.template expand<false>(dst, ref);
+                    if (one)
+                        t.template expand<false>(dst);
                     else
-                        t.template expand<true>(dst, ref);
+                        t.template expand<true>(dst);
                     fence_proxy_async();  // these stores, for the tensor core
                     __syncwarp();
                     // test hook: one warp never signals the first K tile
                     if (lane == 0 && !(fault_skip && !of_v && j == 0))
                         ptx::mbar_arrive(bar((of_v ? C::B_VFULL : C::B_KFULL) + j % C::KST));
-                    if (j + 1 < steps) fetch(j + 1);
+                    if (j + 1 < steps) t.fetch(jbeg + (j + 1) * kBN, jend, dF, nF, p.cache, p.status);
                 }
             } else {
                 TileRows kv{0, 0};  // token rows of key step j, shared by its K and V tiles
@@ -504,39 +497,65 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     ptx::tc_fence_after();
                     issue_s(qd0, 0, tmem + C::COL_S0);
                     ptx::mma_commit(bar(C::B_SFULL + 0));
-                    issue_s(qd1, 0, tmem + C::COL_S1);
-                    ptx::mma_commit(bar(C::B_SFULL + 1));
-                    ptx::mma_commit(bar(C::B_KEMPTY + 0));
                 }
-                for (int j = 0; ok && j < nkv; ++j) {
-                    const int vs = j % C::VST;
-                    const bool v_ok = ptx::mbar_wait(bar(C::B_VFULL + vs), (j / C::VST) & 1, abort, lim);
-                    if (v_ok) fence_proxy_async();
-                    if (!v_ok || !issue_o(0, vs, j > 0, j & 1)) {
-                        ok = false;
-                        break;
+                if (halves) {
+                    // query tile qt works on the key tiles 2 i + qt, each tile's slots released by its
+                    // one reader
+                    auto next_s = [&](int qt, int j) {  // S of key tile j, whose slot it releases
+                        if (!ptx::mbar_wait(bar(C::B_KFULL + j % C::KST), (j / C::KST) & 1, abort, lim)) return false;
+                        fence_proxy_async();
+                        ptx::tc_fence_after();
+                        issue_s(qt ? qd1 : qd0, j % C::KST, tmem + (qt ? C::COL_S1 : C::COL_S0));
+                        ptx::mma_commit(bar(C::B_SFULL + qt));
+                        ptx::mma_commit(bar(C::B_KEMPTY + j % C::KST));
+                        return true;
+                    };
+                    if (ok) ptx::mma_commit(bar(C::B_KEMPTY + 0));
+                    if (ok && nkv > 1) ok = next_s(1, 1);
+                    for (int j = 0; ok && j < nkv; ++j) {
+                        const int qt = j & 1, i = j >> 1, vs = j % C::VST;
+                        ok = ptx::mbar_wait(bar(C::B_VFULL + vs), (j / C::VST) & 1, abort, lim);
+                        if (ok) fence_proxy_async();
+                        ok = ok && issue_o(qt, vs, i > 0, i & 1);
+                        if (ok) ptx::mma_commit(bar(C::B_VEMPTY + vs));
+                        if (ok && j + 2 < nkv) ok = next_s(qt, j + 2);
                     }
-                    const bool more = j + 1 < nkv;
-                    const int ks = (j + 1) % C::KST;
-                    if (more) {
-                        if (!ptx::mbar_wait(bar(C::B_KFULL + ks), ((j + 1) / C::KST) & 1, abort, lim)) {
+                } else {
+                    if (ok) {
+                        issue_s(qd1, 0, tmem + C::COL_S1);
+                        ptx::mma_commit(bar(C::B_SFULL + 1));
+                        ptx::mma_commit(bar(C::B_KEMPTY + 0));
+                    }
+                    for (int j = 0; ok && j < nkv; ++j) {
+                        const int vs = j % C::VST;
+                        const bool v_ok = ptx::mbar_wait(bar(C::B_VFULL + vs), (j / C::VST) & 1, abort, lim);
+                        if (v_ok) fence_proxy_async();
+                        if (!v_ok || !issue_o(0, vs, j > 0, j & 1)) {
                             ok = false;
                             break;
                         }
-                        fence_proxy_async();
-                        ptx::tc_fence_after();
-                        issue_s(qd0, ks, tmem + C::COL_S0);
-                        ptx::mma_commit(bar(C::B_SFULL + 0));
-                    }
-                    if (!issue_o(1, vs, j > 0, j & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::mma_commit(bar(C::B_VEMPTY + vs));
-                    if (more) {
-                        issue_s(qd1, ks, tmem + C::COL_S1);
-                        ptx::mma_commit(bar(C::B_SFULL + 1));
-                        ptx::mma_commit(bar(C::B_KEMPTY + ks));
+                        const bool more = j + 1 < nkv;
+                        const int ks = (j + 1) % C::KST;
+                        if (more) {
+                            if (!ptx::mbar_wait(bar(C::B_KFULL + ks), ((j + 1) / C::KST) & 1, abort, lim)) {
+                                ok = false;
+                                break;
+                            }
+                            fence_proxy_async();
+                            ptx::tc_fence_after();
+                            issue_s(qd0, ks, tmem + C::COL_S0);
+                            ptx::mma_commit(bar(C::B_SFULL + 0));
+                        }
+                        if (!issue_o(1, vs, j > 0, j & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::mma_commit(bar(C::B_VEMPTY + vs));
+                        if (more) {
+                            issue_s(qd1, ks, tmem + C::COL_S1);
+                            ptx::mma_commit(bar(C::B_SFULL + 1));
+                            ptx::mma_commit(bar(C::B_KEMPTY + ks));
+                        }
                     }
                 }
                 if (ok) {
@@ -559,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         const uint32_t s_addr = tmem + lane_base + (qt ? C::COL_S1 : C::COL_S0);
         const uint32_t o_col = qt ? C::COL_O1 : C::COL_O0;
         const uint32_t sfull = bar(C::B_SFULL + qt);
-        const int qi = q_first + qt * kBM + row;
+        const int qi = q_first + (halves ? 0 : qt * kBM) + row;
         const int tq = start + dF.div(min(qi, n_q - 1));
         auto bias_of = [&](int f) { return tab[clamp_dist(tq - ring.time(f), dmax) + dmax]; };
         float m_run = -INFINITY, l_run = 0.f;  // in units of log2
@@ -574,11 +593,12 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 ptx::mbar_arrive(bar(C::B_QF16));
             }
         }
-        for (int j = 0; ok && j < nkv; ++j) {
+        const int tiles = halves ? (nkv - qt + 1) / 2 : nkv;  // of this query tile
+        for (int j = 0; ok && j < tiles; ++j) {
             // Every wait of a softmax warp is made uniform over the warp (a lane can see the abort
             // flag while another sees the phase complete): the tcgen05.ld/st below are
             // .sync.aligned and need all 32 lanes.
-            const int j0 = jbeg + j * kBN;
+            const int j0 = jbeg + (halves ? 2 * j + qt : j) * kBN;
             const int f0 = dF.div(j0);
             const int border = (f0 + 1) * nF - j0;  // tile column where the next frame starts
             float off = bias_of(f0), mul = sl2;     // scores are S * mul + off, in log2
@@ -712,9 +732,31 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             ptx::tc_fence_after();
             // a row without a visible key: 0, and -inf for its log-sum-exp
             const float v_scale = CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f;
-            const float inv_l = l_run == 0.f ? 0.f : v_scale / l_run;
-            const float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run) - (CACHE ? kPShift : 0.f);
-            const bool real = qi < n_q && row_ok(rows(qi), p.nrows, p.status);
+            float inv_l = l_run == 0.f ? 0.f : v_scale / l_run;
+            float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run) - (CACHE ? kPShift : 0.f);
+            float* other = reinterpret_cast<float*>(smem + C::OFF_K) + row;  // [d][128], over the finished K ring
+            float join = 0.f;  // weight of the other half's result
+            if (halves && nkv > 1) {
+                // the second half's result and log-sum-exp go through shared memory to the first
+                if (qt == 1) {
+#pragma unroll
+                    for (int g = 0; g < D / 32; ++g) {
+                        uint32_t ov[32];
+                        ptx::tmem_ld32(tmem + lane_base + o_col + 32 * g, ov);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) other[(32 * g + e) * kBM] = __uint_as_float(ov[e]) * inv_l;
+                    }
+                    tab[row] = l2;  // the softmax is done with the bias
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                const float l2b = tab[row], top = fmaxf(l2, l2b) == -INFINITY ? 0.f : fmaxf(l2, l2b);
+                const float wa = ptx::ex2_approx(l2 - top), wb = ptx::ex2_approx(l2b - top), sum = wa + wb;
+                inv_l *= sum == 0.f ? 0.f : wa / sum;
+                join = sum == 0.f ? 0.f : wb / sum;
+                l2 = sum == 0.f ? -INFINITY : top + ptx::lg2_approx(sum);
+            }
+            const bool real = qi < n_q && !(halves && qt == 1) && row_ok(rows(qi), p.nrows, p.status);
             const size_t grow = real ? static_cast<size_t>(rows(qi)) : 0;
             if (real) {
                 if (p.splits > 1)
@@ -732,13 +774,19 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
 #pragma unroll
                     for (int e = 0; e < 32; ++e) ov[e] = 0u;
                 }
+                if (halves && nkv > 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), inv_l, join * other[(32 * g + e) * kBM]));
+                }
+                const float inv = halves && nkv > 1 ? 1.f : inv_l;
                 if (p.splits > 1) {
                     if (real) {
                         float4* dst = reinterpret_cast<float4*>(p.part_o + (grow * p.splits + split) * D + 32 * g);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv_l, __uint_as_float(ov[4 * e + 1]) * inv_l,
-                                                 __uint_as_float(ov[4 * e + 2]) * inv_l, __uint_as_float(ov[4 * e + 3]) * inv_l);
+                            dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
+                                                 __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
                     }
                 } else {
                     auto store = [&](uint16_t* to, const uint32_t(&w)[16]) {
@@ -750,14 +798,14 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     uint32_t pkd[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        pkd[e] = ptx::pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
+                        pkd[e] = ptx::pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
                     if (real) store(p.out, pkd);
                     if (!CACHE && p.out_lo) {  // what the rounding took: exact in fp32, rounded once
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             pkd[e] = ptx::pack_bf16x2(
-                                fmaf(__uint_as_float(ov[2 * e]), inv_l, -__uint_as_float(pkd[e] << 16)),
-                                fmaf(__uint_as_float(ov[2 * e + 1]), inv_l, -__uint_as_float(pkd[e] & 0xffff0000u)));
+                                fmaf(__uint_as_float(ov[2 * e]), inv, -__uint_as_float(pkd[e] << 16)),
+                                fmaf(__uint_as_float(ov[2 * e + 1]), inv, -__uint_as_float(pkd[e] & 0xffff0000u)));
                         if (real) store(p.out_lo, pkd);
                     }
                 }
@@ -839,7 +887,8 @@ int launch_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
     const long long n_max = static_cast<long long>(g.T) * max_class_tokens(g);
-    const dim3 grid(static_cast<unsigned>((n_max + 2 * kBM - 1) / (2 * kBM) * p.splits), g.heads, g.B * g.Ph * g.Pw);
+    const int rows = p.halves ? kBM : 2 * kBM;
+    const dim3 grid(static_cast<unsigned>((n_max + rows - 1) / rows * p.splits), g.heads, g.B * g.Ph * g.Pw);
     skiparse_attn_frames_kernel<D, CACHE><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return static_cast<int>(e);
@@ -853,21 +902,35 @@ int launch_kind(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream
 
 }  // namespace
 
+// Whether 128-query CTAs, whose two softmax groups share the keys, finish a call of n queries and
+// `keys` keys a class earlier than 256-query CTAs: by waves of one CTA per SM (148) times key steps,
+// with three steps' worth for a CTA's start and end. One query tile alone always goes that way.
+// Larger calls keep to 256 queries unless it gains a tenth: there each key tile is loaded half as often.
+bool frames_halves(const Geometry& g, long long n, long long keys) {
+    if (n <= kBM) return true;
+    const long long pairs = static_cast<long long>(g.heads) * g.B * g.Ph * g.Pw, steps = (keys + kBN - 1) / kBN;
+    auto waves = [&](long long rows) { return ((n + rows - 1) / rows * pairs + 147) / 148; };
+    // a step of two key tiles takes 1.5 times a step of one at d = 128, where the loads bound it
+    return 10 * waves(kBM) * ((steps + 1) / 2 * (g.d == 128 ? 3 : 2) + 6) < 9 * waves(2 * kBM) * (2 * steps + 6);
+}
+
 // Splits of the key range: enough CTAs for one per SM (148) from a call with fewer, as long as
 // each part keeps at least four key tiles. The cache's capacity stands for its length, which
 // only the device knows.
 int cached_splits(const Geometry& g, int cap) {
     if (cached_small(g)) return cached_small_splits(g, cap);
-    const long long nF = max_class_tokens(g);
-    const long long ctas = (g.T * nF + 2 * kBM - 1) / (2 * kBM) * g.heads * g.B * g.Ph * g.Pw;
-    const long long tiles = (cap * nF + kBN - 1) / kBN;
+    const long long n = static_cast<long long>(g.T) * max_class_tokens(g), keys = static_cast<long long>(cap) * max_class_tokens(g);
+    const long long rows = frames_halves(g, n, keys) ? kBM : 2 * kBM;
+    const long long ctas = (n + rows - 1) / rows * g.heads * g.B * g.Ph * g.Pw, tiles = (keys + kBN - 1) / kBN;
     long long s = 148 / ctas;
     if (s > tiles / 4) s = tiles / 4;
     return static_cast<int>(s < 1 ? 1 : s);
 }
 
-int launch_frames_fwd(const FramesFwdParams& p, const Geometry& g, void* stream) {
+int launch_frames_fwd(FramesFwdParams p, const Geometry& g, void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    p.halves = frames_halves(g, static_cast<long long>(g.T) * max_class_tokens(g),
+                             static_cast<long long>(p.cache.k ? p.cache.cap : g.T) * max_class_tokens(g));
     if (p.cache.k && cached_small(g)) {
         const int e = launch_cached_small(p, g, stream);
         return e || p.splits == 1 ? e : launch_frames_join(p, g.d, st);

@@ -63,6 +63,7 @@ struct FramesFwdParams {
     FrameBias bias;
     CacheView cache;
     int splits;
+    int halves;       // 128-query CTAs; chosen by launch_frames_fwd
     float scale_log2;
     unsigned long long wait_limit_ns;
     int fault;
@@ -110,7 +111,7 @@ struct AppendParams {
 };
 
 // Launchers. They return the cudaError_t as int.
-int launch_frames_fwd(const FramesFwdParams& p, const Geometry& g, void* stream);
+int launch_frames_fwd(FramesFwdParams p, const Geometry& g, void* stream);
 int launch_frames_bwd(const FramesBwdParams& p, const Geometry& g, void* stream);
 int launch_cache_append(const AppendParams& p, const Geometry& g, int d, void* stream);
 // Attention of few queries over the cache: whether a call's classes are small enough for it, its
