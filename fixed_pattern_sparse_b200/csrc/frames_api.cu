@@ -155,7 +155,7 @@ int relbias_bwd(int dims, const void* q, const void* k, const void* v, const voi
     p.dout = static_cast<const uint16_t*>(dout);
     p.lse = lse;
     p.delta = reinterpret_cast<float*>(ws);
-    p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+    p.nlse2 = reinterpret_cast<float*>(ws + w.lse2);
     p.bias2 = reinterpret_cast<float*>(ws + w.bias2);
     p.part = reinterpret_cast<float*>(ws + w.part);
     p.dtable = static_cast<uint16_t*>(dtable);

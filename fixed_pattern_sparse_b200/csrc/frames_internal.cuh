@@ -24,12 +24,12 @@ struct FrameBias {
 };
 
 // The dimensions of a call, filled from Geometry, and the divisions that the kernels need: by the
-// rows, columns and tokens per frame of each class and by the class counts. (Their constants take a
+// rows, columns, tokens per frame and 32-token chunks per frame of each class, and by the class counts. (Their constants take a
 // thread a 64-bit division each; in small calls those were a good part of the kernel's time.)
 struct FrameGeom {
     int T, H, W, heads, Ph, Pw, mode;
     int Rc[kMaxAxisClasses], Sc[kMaxAxisClasses];
-    FastDiv dR[kMaxAxisClasses], dS[kMaxAxisClasses], dF[kMaxAxisClasses], dPh, dPw;
+    FastDiv dR[kMaxAxisClasses], dS[kMaxAxisClasses], dF[kMaxAxisClasses], dC[kMaxAxisClasses], dPh, dPw;
 };
 
 // The e4m3 frame cache of one layer: codes (B*classes, heads, cap, F, d), F the padded tokens
@@ -79,7 +79,7 @@ struct FramesBwdParams {
     const uint16_t* dout;
     const float* lse;
     float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo))
-    float* lse2;       // workspace (rows): lse * log2(e), at least kLse2Low
+    float* nlse2;      // workspace (rows): -lse * log2(e), at most -kLse2Low
     float* bias2;      // workspace (heads, 2D+1): bias * log2(e), -inf where masked
     float* part;       // workspace (heads, seqs, tiles, ND): sums of dS by frame distance
     uint16_t* dtable;  // bf16 (NB, heads)
@@ -139,7 +139,9 @@ inline void fill_frame_geom(FrameGeom& f, const Geometry& g) {
         f.Sc[c] = g.Sc[c];
         f.dR[c].init(g.Rc[c]);
         f.dS[c].init(g.Sc[c]);
-        if (c < g.Ph * g.Pw) f.dF[c].init(g.Rc[c / g.Pw] * g.Sc[c % g.Pw]);
+        const int nF = c < g.Ph * g.Pw ? g.Rc[c / g.Pw] * g.Sc[c % g.Pw] : 0;
+        f.dF[c].init(nF);
+        f.dC[c].init((nF + 31) / 32);
     }
     f.dPh.init(g.Ph);
     f.dPw.init(g.Pw);
