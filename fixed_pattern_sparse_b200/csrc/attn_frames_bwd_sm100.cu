@@ -640,12 +640,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         ptx::tmem_dealloc(tmem, C::NCOLS);
     }
     if (KV) {  // this CTA's sums by distance, its warps' tables added in order
-        float* part = p.part + ((static_cast<size_t>(head) * p.seqs + seq) * p.tiles + tile) * p.ND;
+        const size_t n = static_cast<size_t>(p.seqs) * p.tiles;
+        float* part = p.part + static_cast<size_t>(head) * p.ND * n + static_cast<size_t>(seq) * p.tiles + tile;
         for (int u = threadIdx.x; u < p.ND; u += kBwdThreads) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) s += hist[w * p.ND + u];
-            part[u] = s;
+            part[u * n] = s;
         }
     }
 }
@@ -688,28 +689,34 @@ __global__ void __launch_bounds__(256) skiparse_frames_stats_kernel(const Frames
         p.bias2[i] = bias_log2(p.bias, p.g.heads, static_cast<int>(i % entries), static_cast<int>(i / entries));
 }
 
-// dtable of one head: the workspace's rows added per distance (one warp each), then the distances of
-// each bucket.
-__global__ void __launch_bounds__(512) skiparse_frames_dtable_kernel(const FramesBwdParams p) {
+// dtable of one head: the CTAs' sums added per distance (one warp each), then the distances of each
+// bucket.
+constexpr int kTableThreads = 1024;
+__global__ void __launch_bounds__(kTableThreads) skiparse_frames_dtable_kernel(const FramesBwdParams p) {
     __shared__ float sums[kMaxDistEntries];
+    __shared__ int tiles_of[kMaxAxisClasses];  // key tiles of each class; the others were not launched
     const int head = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q2 = p.g.Ph * p.g.Pw;
-    const float* part = p.part + static_cast<size_t>(head) * p.seqs * p.tiles * p.ND;
-    for (int u = warp; u < p.ND; u += 16) {
+    if (threadIdx.x < q2) {
+        const int c = threadIdx.x;
+        tiles_of[c] = (p.g.T * p.g.Rc[c / p.g.Pw] * p.g.Sc[c % p.g.Pw] + kTileRows - 1) / kTileRows;
+    }
+    __syncthreads();
+    const int n = p.seqs * p.tiles;
+    const float* part = p.part + static_cast<size_t>(head) * p.ND * n;
+    for (int u = warp; u < p.ND; u += kTableThreads / 32) {
         float s = 0.f;
-        for (int seq = 0; seq < p.seqs; ++seq) {
-            const int c = seq % q2;
-            const int n_c = p.g.T * p.g.Rc[c / p.g.Pw] * p.g.Sc[c % p.g.Pw];
-            const int tiles = (n_c + kTileRows - 1) / kTileRows;  // the others were not launched
-            for (int t = lane; t < tiles; t += 32) s += part[(static_cast<size_t>(seq) * p.tiles + t) * p.ND + u];
+        for (int i = lane; i < n; i += 32) {
+            const int seq = i / p.tiles;
+            if (i - seq * p.tiles < tiles_of[seq % q2]) s += part[static_cast<size_t>(u) * n + i];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) sums[u] = s;
     }
     __syncthreads();
-    for (int g = threadIdx.x; g < p.bias.NB; g += 512) {
+    for (int g = threadIdx.x; g < p.bias.NB; g += kTableThreads) {
         float s = 0.f;
         for (int u = 0; u < p.ND; ++u)
             if (p.bias.buckets[u - p.Dn + p.bias.D] == g) s += sums[u];
@@ -739,9 +746,9 @@ int launch_bwd_d(const FramesBwdParams& p, const Geometry& g, cudaStream_t strea
 
 // Whether the key-major kernel streams its queries in 32-row chunks of one frame each (the last of
 // a frame filled up): no chunk then holds a frame's border, whose handling costs the kernel
-// registers everywhere, for at most a quarter more rows. 480p (390 tokens a frame, 7 % more):
-// 3.77 ms with borders, 3.45 ms without.
-bool aligned_chunks(int nF) { return (nF + 31) / 32 * 32 * 4 <= nF * 5; }
+// registers everywhere, for up to twice the rows. 480p (390 tokens a frame, 7 % more rows): 3.77 ms
+// with borders, 3.45 without; 20 tokens a frame (60 % more), 4 x 16 frames: 84 us with borders, 60 without.
+bool aligned_chunks(int nF) { return (nF + 31) / 32 * 32 <= nF * 2; }
 
 template <int D>
 int launch_bwd_all(const FramesBwdParams& p, const Geometry& g, cudaStream_t st) {
@@ -759,7 +766,7 @@ int launch_bwd_all(const FramesBwdParams& p, const Geometry& g, cudaStream_t st)
     if (e) return e;
     e = launch_bwd_d<D, false, false>(p, g, st);
     if (e) return e;
-    skiparse_frames_dtable_kernel<<<g.heads, 512, 0, st>>>(p);
+    skiparse_frames_dtable_kernel<<<g.heads, kTableThreads, 0, st>>>(p);
     return static_cast<int>(cudaGetLastError());
 }
 

@@ -89,8 +89,8 @@ int relbias_fwd(int dims, const void* q, const void* k, const void* v, const voi
 }
 
 // Workspace of the backward pass, in order (each part 256-byte aligned): D and lse * log2(e) of
-// every row, the bias by head and distance, the sums of dS by head, subsequence, key tile and
-// distance.
+// every row, the bias by head and distance, the sums of dS by head, distance, subsequence and
+// key tile.
 struct BwdSpace {
     size_t lse2, bias2, part, bytes;
     int Dn, ND, tiles;

@@ -81,7 +81,7 @@ struct FramesBwdParams {
     float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo))
     float* nlse2;      // workspace (rows): -lse * log2(e), at most -kLse2Low
     float* bias2;      // workspace (heads, 2D+1): bias * log2(e), -inf where masked
-    float* part;       // workspace (heads, seqs, tiles, ND): sums of dS by frame distance
+    float* part;       // workspace (heads, ND, seqs, tiles): sums of dS by frame distance
     uint16_t* dtable;  // bf16 (NB, heads)
     uint16_t* dq;
     uint16_t* dk;
