@@ -14,8 +14,11 @@
 //     chooses between two; frames of fewer than 32 tokens look the bias up where it changes.
 //     Streamed tiles that no stationary row can see are skipped.
 //   * D. Every row of dS sums to zero over its keys, so an error of D_i enters the bias gradient
-//     through all of the row's keys with one sign. D from the bf16 output would dominate that
-//     gradient's error; the forward can therefore store what rounding its output took (out_lo).
+//     through all of the row's keys with one sign, and D from the forward's output, which carries
+//     the roundings of P and of the output itself, would dominate that gradient's error. The
+//     query-major kernel therefore runs first, with that D, and sums its rows of dS: what is left
+//     is D's error, and the key-major kernel gets D without it. (dQ keeps D's error, the smaller
+//     for a stored rounding residual of the output, out_lo.)
 //   * Bias gradient. The key-major kernel sums dS, in fp32, before its rounding to bf16, in a
 //     register per key row for as long as the streamed queries stay in one frame; when the
 //     frame changes, the warp adds its rows of equal distance by shuffles and one lane adds the
@@ -23,7 +26,7 @@
 //     eight tables, in a fixed order, to the workspace, and the last kernel adds those rows and
 //     joins distances to buckets, in a fixed order too: the result does not depend on timing.
 //     Per score this costs one addition (half of one packed instruction).
-// Launches: row statistics (D, L in log2, the bias by head and distance), dK/dV, dQ, dtable.
+// Launches: row statistics (D, L in log2, the bias by head and distance), dQ, dK/dV, dtable.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -389,6 +392,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         float acc = 0.f;   // sum of dS over the queries of frame f_acc so far
         int f_acc = -1;
         float row_l2 = 0.f, row_d = 0.f;
+        float2 row_sum = make_float2(0.f, 0.f);  // query-major: of the row's dS
         bool ok = true;
         // the frame of the next column, the columns until the frame after it starts, and the bias
         int f = AL ? f_lo : dF.div(jbeg + 64 * h), next = (f + 1) * nF - (jbeg + 64 * h);
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
                         const float2 sv = ds_pair(make_float2(pr[32 * g + c], pr[32 * g + c + 1]),
                                                   make_float2(dcol[2 * e], dcol[2 * e + 1]), dv[c], dv[c + 1]);
                         pk[4 * e4 + e] = ptx::pack_bf16x2(sv.x, sv.y);
-                        if (KV) sum = __fadd2_rn(sum, sv);
+                        sum = __fadd2_rn(sum, sv);
                         if (KV && !AL) {
                             dv[c] = __float_as_uint(sv.x);
                             dv[c + 1] = __float_as_uint(sv.y);
@@ -586,6 +590,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
                     }
                     ends -= 32;
                 }
+                if (!KV) row_sum = __fadd2_rn(row_sum, sum);
                 ptx::tmem_st16(x2 + 16 * g, pk);
             }
             ptx::tmem_wait_st();
@@ -600,6 +605,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
             const int si = first + row;                 // stationary row (key or query)
             const bool store = si < n_c && row_ok(rows(si), p.nrows, p.status);
             const size_t grow = store ? static_cast<size_t>(rows(si)) : 0;
+            if (!KV && nstream > 0) {
+                // The row's dS ought to sum to zero; what it sums to is D's error, which goes into D
+                // for the key-major kernel.
+                float* other = reinterpret_cast<float*>(smem + C::OFF_VEC) + row;  // over the rows' L, long read
+                if (h == 1) *other = row_sum.x + row_sum.y;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (h == 0 && store) p.delta[grow] = row_d + ((row_sum.x + row_sum.y) + *other);
+            }
             constexpr int HALF = D / 2;                 // accumulator columns of this warpgroup
             // key-major: acc1 = dV (unscaled), acc2 = dK ; query-major: acc1 = dQ
 #pragma unroll
@@ -762,9 +775,9 @@ int launch_bwd_all(const FramesBwdParams& p, const Geometry& g, cudaStream_t st)
     skiparse_frames_stats_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p, nrows);
     int e = static_cast<int>(cudaGetLastError());
     if (e) return e;
-    e = aligned_chunks(max_class_tokens(g)) ? launch_bwd_d<D, true, true>(p, g, st) : launch_bwd_d<D, true, false>(p, g, st);
-    if (e) return e;
     e = launch_bwd_d<D, false, false>(p, g, st);
+    if (e) return e;
+    e = aligned_chunks(max_class_tokens(g)) ? launch_bwd_d<D, true, true>(p, g, st) : launch_bwd_d<D, true, false>(p, g, st);
     if (e) return e;
     skiparse_frames_dtable_kernel<<<g.heads, kTableThreads, 0, st>>>(p);
     return static_cast<int>(cudaGetLastError());

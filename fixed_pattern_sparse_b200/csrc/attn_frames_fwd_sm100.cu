@@ -276,9 +276,10 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int nF = cls.nF;
     const FastDiv dF = cls.dF;
     const int n_q = p.g.T * nF;
-    const bool halves = p.halves;  // both tiles are the same 128 queries, each over half of the key tiles
-    const int q_first = pair * (halves ? kBM : 2 * kBM);
+    const int q_first = pair * (p.halves ? kBM : 2 * kBM);
     if (q_first >= n_q) return;  // uniform over the CTA, before any shared state
+    // both tiles are the same 128 queries, each over half of the key tiles; so is a class's rest
+    const bool halves = p.halves || n_q - q_first <= kBM;
     int start = 0;
     if (CACHE) {
         start = p.cache.start[cls.b];
@@ -594,7 +595,16 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             }
         }
         const int tiles = halves ? (nkv - qt + 1) / 2 : nkv;  // of this query tile
-        for (int j = 0; ok && j < tiles; ++j) {
+        int done = 0;
+        if (!__any_sync(0xffffffffu, qi < n_q)) {
+            // All 32 rows of the warp lie past the class's end: it leaves their S as it is (rows of P and
+            // O do not mix) and only keeps the barriers going.
+            for (; ok && done < tiles; ++done) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(sfull, done & 1, abort, lim));
+                for (int h = 0; ok && h < kPParts; ++h) ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + h));
+            }
+        }
+        for (int j = done; ok && j < tiles; ++j) {
             // Every wait of a softmax warp is made uniform over the warp (a lane can see the abort
             // flag while another sees the phase complete): the tcgen05.ld/st below are
             // .sync.aligned and need all 32 lanes.

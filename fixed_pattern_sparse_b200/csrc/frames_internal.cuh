@@ -78,7 +78,7 @@ struct FramesBwdParams {
     const uint16_t* out_lo;  // optional
     const uint16_t* dout;
     const float* lse;
-    float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo))
+    float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo)), then corrected by the dQ kernel
     float* nlse2;      // workspace (rows): -lse * log2(e), at most -kLse2Low
     float* bias2;      // workspace (heads, 2D+1): bias * log2(e), -inf where masked
     float* part;       // workspace (heads, ND, seqs, tiles): sums of dS by frame distance

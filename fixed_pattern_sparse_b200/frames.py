@@ -213,7 +213,7 @@ def skiparse1d_attn_relbias_fwd(q, k, v, table, buckets, P: int, mode: int, out=
 def skiparse2d_attn_relbias_bwd(q, k, v, out, dout, lse, table, buckets, P: int, mode: int, dq=None, dk=None, dv=None,
                                 dtable=None, out_lo=None, workspace=None, stream=None):
     """Backward pass of skiparse2d_attn_relbias_fwd: returns (dq, dk, dv, dtable). `out_lo`: the
-    forward's, if it stored one (the gradient of the table gains most). `workspace`: an optional CUDA
+    forward's, if it stored one (for a more exact dq). `workspace`: an optional CUDA
     uint8 tensor of skiparse2d_attn_relbias_bwd_workspace_bytes() bytes."""
     return _relbias_bwd(2, q, k, v, out, dout, lse, table, buckets, P, mode, dq, dk, dv, dtable, out_lo, workspace,
                         stream)

@@ -302,8 +302,8 @@ SKIPARSE_API int skiparse1d_attn_relbias_fwd(const void* q, const void* k, const
 /*
  * Its backward pass: dq, dk, dv as skiparse2d_attn_bwd, with P from the biased, masked scores, and
  *   out_lo : the forward's, or NULL. With it D = rowsum(dout o out) keeps the precision that bf16
- *            takes from out; the error of dtable is then about that of its own rounding, without
- *            it up to a few times that.
+ *            takes from out, and so does dq. (dk, dv and dtable do not depend on it: the row sums
+ *            of dS correct D for them.)
  *   dtable : (num_buckets, heads) bf16, written entirely: dtable[g][head] = sum of dS over all
  *            pairs of the batch in bucket g (summed in fp32, rounded once). A masked entry of the
  *            table and a bucket that no pair falls in get 0. Must not overlap table.
@@ -312,7 +312,7 @@ SKIPARSE_API int skiparse1d_attn_relbias_fwd(const void* q, const void* k, const
  *            and nothing in it is used after the call. Calls that can run at the same time (on
  *            other streams, or as replays of graphs captured separately) need workspaces of
  *            their own.
- * Four kernel launches (row statistics, dk/dv, dq, dtable), no atomics on results: deterministic.
+ * Four kernel launches (row statistics, dq, dk/dv, dtable), no atomics on results: deterministic.
  */
 SKIPARSE_API int skiparse2d_attn_relbias_bwd(const void* q, const void* k, const void* v, const void* out,
                                              const void* out_lo, const void* dout, const float* lse,

@@ -55,9 +55,10 @@ def reference(q, k, v, table, buckets, P, mode, dims=2, dout=None, exact_d=True)
     """out, lse, (dq, dk, dv, dtable) in fp64 with the bound on each one's error, as a dict
     name -> (value, tolerance). The bounds count roundings: P and dS enter their products as bf16
     (half a step each), results are rounded to bf16 once; 2^-13 covers the fp32 arithmetic between
-    (scores, exponentials, differences). D = dout . out is taken from the forward's out, whose error
-    is that of P in P V, (e + 2^-13) P|V|, and its own rounding, e |out|, or e^2 of it where the
-    residual is passed (rounded once itself, hence 2 e^2): |dout| times that is D's error."""
+    (scores, exponentials, differences). For dq, D = dout . out is taken from the forward's out, whose
+    error is that of P in P V, (e + 2^-13) P|V|, and its own rounding, e |out|, or e^2 of it where
+    the residual is passed (rounded once itself, hence 2 e^2): |dout| times that is D's error. For
+    dk and dtable D is corrected by the fp32 sum of its row of dS."""
     B, T, H, W, h, d = q.shape
     dev, n = q.device, H * W
     cls = token_classes(H, W, P, mode, dims).to(dev).repeat(T)
@@ -84,9 +85,11 @@ def reference(q, k, v, table, buckets, P, mode, dims=2, dout=None, exact_d=True)
         ds = p * (dp - (p * dp).sum(-1, keepdim=True))
         o_err = (e + fine) * torch.einsum("hqk,khd->qhd", p, vb.abs()) + (e * e * 2 if exact_d else e) * o.abs()
         e_d = torch.einsum("qhd,qhd->hq", do.abs(), o_err)[..., None]
-        e_ds = p * e_d + fine * p * (dp.abs() + (p * dp).sum(-1, keepdim=True).abs())
+        mean = (p * dp.abs()).sum(-1, keepdim=True)
+        e_ds = fine * p * (dp.abs() + mean)
         rows = e_ds + e * ds.abs()
-        for m, val, bound in (("dq", torch.einsum("hqk,khd->qhd", ds, kb) * sc, torch.einsum("hqk,khd->qhd", rows, kb.abs()) * sc),
+        rows_q = rows + p * e_d
+        for m, val, bound in (("dq", torch.einsum("hqk,khd->qhd", ds, kb) * sc, torch.einsum("hqk,khd->qhd", rows_q, kb.abs()) * sc),
                               ("dk", torch.einsum("hqk,qhd->khd", ds, qb) * sc, torch.einsum("hqk,qhd->khd", rows, qb.abs()) * sc),
                               ("dv", torch.einsum("hqk,qhd->khd", p, do), torch.einsum("hqk,qhd->khd", (e + fine) * p, do.abs()))):
             got[m].append(val)

@@ -52,6 +52,8 @@ SHAPES = [
     ((2, 4, 5, 7, 2, 128), 2, 0, 1, (9, 6, True, 3)),
     ((1, 2, 33, 34, 1, 32), 8, 1, 2, (3, 2, False, None)),     # 64 classes, some empty
     ((1, 2, 20, 31, 1, 128), 1, 0, 2, (4, 1, True, None)),     # frames of 620: whole tiles hidden
+    ((1, 1, 12, 17, 2, 64), 1, 0, 2, (3, 2, False, None)),     # one frame, one bucket: dtable is 0 but for fp32
+    ((1, 3, 9, 15, 2, 64), 1, 0, 2, (4, 2, True, None)),       # 405 queries: a last CTA of 149
 ]
 IDS = ["x".join(map(str, s[0])) + f"_p{s[1]}m{s[2]}d{s[3]}" for s in SHAPES]
 
@@ -322,6 +324,8 @@ READS = [
     ((1, 1, 40, 50, 1, 64), 2, 0, 2, 12, [11], (9, 12, True, None)),
     ((1, 1, 4, 4, 2, 64), 1, 0, 2, 300, [299], None),                         # 16 tokens a frame
     ((1, 1, 17, 1, 1, 128), 1, 0, 2, 200, [120], (9, 12, True, None)),        # 17 tokens a frame
+    ((1, 2, 13, 12, 1, 64), 1, 0, 2, 8, [6], (9, 12, True, None)),            # 312 queries: a last CTA of 56
+    ((1, 1, 20, 20, 1, 128), 1, 1, 2, 9, [20], None),                         # 400 queries: of 144
 ]
 
 
