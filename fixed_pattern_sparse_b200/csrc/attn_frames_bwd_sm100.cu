@@ -476,16 +476,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
                                 fmaf(__uint_as_float(xv[32 * g + e]), sl2, (e < next ? off : o1) + (KV ? col_l[32 * g + e] : row_l2)));
                         off = o1;
                         next += nF;
-                    } else {
+                    } else {  // frames of fewer tokens: a lookup per column
+                        const int jg = j0 + 32 * g;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (e == next) {
-                                next += nF;
-                                off = bias_of(++f);
-                            }
-                            pr[32 * g + e] = ptx::ex2_approx(
-                                fmaf(__uint_as_float(xv[32 * g + e]), sl2, off + (KV ? col_l[32 * g + e] : row_l2)));
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            pr[32 * g + e] = ptx::ex2_approx(fmaf(__uint_as_float(xv[32 * g + e]), sl2,
+                                                                  bias_of(dF.div(jg + e)) + (KV ? col_l[32 * g + e] : row_l2)));
+                        f = dF.div(jg + 32);
+                        next = (f + 1) * nF - jg;
+                        off = bias_of(f);
                     }
                     next -= 32;
                 }

@@ -339,6 +339,14 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::NCOLS);
         ptx::tmem_relinquish();
     }
+    // Q starts to travel before the barriers stand; its copies arrive on theirs below
+    const bool q_producer = warp == kProdWarp0 || warp == kProdWarp0 + 1;
+    if (q_producer) {
+        const int pw = warp - kProdWarp0;
+        load_tile<D>(sbase + C::OFF_Q, p.q, rows, q_first, n_q, pw, lane, p.nrows, p.status);
+        load_tile<D>(sbase + C::OFF_Q + C::TILE_BYTES, p.q, rows, halves ? q_first : q_first + kBM, n_q, pw, lane, p.nrows,
+                     p.status);
+    }
     // the bias by distance, and the first and last distance that is visible
     int dlo, dhi;
     fill_bias(tab, p.bias, p.g.heads, head, C::THREADS, dlo, dhi);
@@ -408,12 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     w_ok = ptx::mbar_wait(bar((is_v ? C::B_VEMPTY : C::B_KEMPTY) + j % nst), ((j / nst) - 1) & 1, abort, lim);
                 return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
             };
-            if (nkv > 0 && pw < 2 && !of_v) {
-                load_tile<D>(sbase + C::OFF_Q, p.q, rows, q_first, n_q, pw, lane, p.nrows, p.status);
-                load_tile<D>(sbase + C::OFF_Q + C::TILE_BYTES, p.q, rows, halves ? q_first : q_first + kBM, n_q, pw,
-                             lane, p.nrows, p.status);
-                cp_async_arrive_noinc(bar(C::B_Q));
-            }
+            if (q_producer) cp_async_arrive_noinc(bar(C::B_Q));
             if constexpr (CACHE) {
                 static_assert(C::KST == C::VST, "one slot index for both rings");
                 CacheTile<D> t;
@@ -637,15 +640,14 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                             sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, e < next ? off : o1));
                         off = o1;
                         next += nF;
-                    } else {
+                    } else {                        // frames of fewer tokens: a lookup per score
+                        const int jg = j0 + 32 * g;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (e == next) {
-                                next += nF;
-                                off = bias_of(++f);  // columns past the last frame are masked below
-                            }
-                            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, off));
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, bias_of(dF.div(jg + e))));
+                        f = dF.div(jg + 32);
+                        next = (f + 1) * nF - jg;
+                        off = bias_of(f);           // (columns past the last frame are masked below)
                     }
                     next -= 32;
                     ptx::tmem_st16(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
