@@ -16,8 +16,8 @@
 //     w = 2^(s + e - mv) with a running maximum mv of s + e of its own, beside p = 2^(s - m) for the
 //     row sum. So P V needs no common scale, and f16 holds every weight down to 2^-31 of the
 //     largest; out = O 2^(mv - m) / l.
-//   * Copies go by cp.async into a ring of four stages per warp that only the copying lane
-//     reads: no barrier in the loop, 16 KB in flight per warp at d = 128.
+//   * Copies go by cp.async into a ring of three stages per warp that only the copying lane
+//     reads: no barrier in the loop, 8 KB in flight per warp at d = 128.
 // What bounds it: reading the cache, as long as a step's instructions (conversions foremost: 64 per
 // lane and step at d = 128, 4 clocks each) keep below the 180 clocks in which an SM's share
 // of HBM delivers its 4 KB.
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kKeys = 16;      // keys of a warp step
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kMaxRows = 32;   // queries per class up to which this kernel is used (measured, 57,000 keys,
                                // d = 128: 30 queries 0.49 ms against the tcgen05 kernel's 0.80, 64: 0.89, 0.52)
 constexpr float kRescaleLog2 = 8.0f;
@@ -55,7 +55,7 @@ struct SmallCfg {
     static constexpr int VB = D / 8;                  // bytes of a lane's copy of a value
     static constexpr int KSTEPS = D / 16;
     static constexpr int MT = D / 16;                 // row tiles of O^T
-    static constexpr int CTAS = NQ == 4 ? 2 : 3;      // per SM, by registers
+    static constexpr int CTAS = NQ == 4 ? 2 : NQ == 2 ? 3 : 4;  // per SM, by registers
 };
 
 template <int BYTES>
@@ -458,13 +458,14 @@ int launch_small(const FramesFwdParams& p, const Geometry& g, cudaStream_t strea
 
 bool cached_small(const Geometry& g) { return static_cast<long long>(g.T) * max_class_tokens(g) <= kMaxRows; }
 
-// One wave of CTAs, of at least 512 keys each (measured: 2 to 3 times as many CTAs cost up to a fifth
-// in small calls and change nothing in large ones).
+// One wave of CTAs for up to 16 queries a class, two for up to 32, of at least 512 keys each (measured:
+// more CTAs cost up to a quarter in small calls and gain nothing in large ones).
 int cached_small_splits(const Geometry& g, int cap) {
-    const long long n = static_cast<long long>(g.T) * max_class_tokens(g), rows = 8 * query_tiles(n);
+    const long long n = static_cast<long long>(g.T) * max_class_tokens(g);
+    const int tiles = query_tiles(n), rows = 8 * tiles;
     const long long keys = static_cast<long long>(cap) * max_class_tokens(g);
     const long long ctas = (n + rows - 1) / rows * g.heads * g.B * g.Ph * g.Pw;
-    long long s = 3 * 148 / ctas;
+    long long s = 148LL * (tiles == 2 ? 3 : 4) / ctas;
     if (s > keys / 512) s = keys / 512;
     return static_cast<int>(s < 1 ? 1 : s);
 }

@@ -161,6 +161,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::NCOLS);
         ptx::tmem_relinquish();
     }
+    // stationary tiles: (K, V) for the key-major kernel, (Q, dO) for the query-major one. They start
+    // to travel before the barriers stand; the copies arrive on theirs below.
+    const uint16_t* g_a1 = KV ? p.k : p.q;
+    const uint16_t* g_a2 = KV ? p.v : p.dout;
+    const uint16_t* g_b1 = KV ? p.q : p.k;
+    const uint16_t* g_b2 = KV ? p.dout : p.v;
+    if (warp >= kBwdProd0 && warp < kBwdProd0 + 4) {
+        const int pair = (warp - kBwdProd0) >> 1, pw = (warp - kBwdProd0) & 1;
+        const TileRows ta = tile_rows(rows, first, n_c, pw, lane, p.nrows, p.status);
+        load_tile_rows<D>(sbase + (pair ? C::OFF_A2 : C::OFF_A1), pair ? g_a2 : g_a1, ta, pw, lane);
+        if (!KV && pair == 0) {  // the stationary queries' L and D
+            load_vec(sbase + C::OFF_VEC, p.nlse2, ta, pw, lane);
+            load_vec(sbase + C::OFF_VEC + 4 * kTileRows, p.delta, ta, pw, lane);
+        }
+    }
     if (KV)
         for (int i = threadIdx.x; i < 8 * p.ND; i += kBwdThreads) hist[i] = 0.f;
     int dlo = dmax + 1, dhi = -dmax - 1;  // first and last visible distance
@@ -207,12 +222,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         return (f_lo + f) * nF + min((q - f * cpf) * 32 + i, nF - 1);
     };
 
-    // stationary tiles: (K, V) for the key-major kernel, (Q, dO) for the query-major one
-    const uint16_t* g_a1 = KV ? p.k : p.q;
-    const uint16_t* g_a2 = KV ? p.v : p.dout;
-    const uint16_t* g_b1 = KV ? p.q : p.k;
-    const uint16_t* g_b2 = KV ? p.dout : p.v;
-
     if (warp >= kBwdProd0 && warp < kBwdProd0 + 4) {
         // ------------------------------------------------------------------ producers
         // Pair 0 (warps 8-9) copies the first streamed tensor (and the L/D statistics), pair 1
@@ -220,15 +229,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         const int pair = (warp - kBwdProd0) >> 1;
         const int pw = (warp - kBwdProd0) & 1;
         const int ns = pair ? C::NS2 : C::NS1;
-        if (nstream > 0) {
-            const TileRows ta = tile_rows(rows, first, n_c, pw, lane, p.nrows, p.status);
-            load_tile_rows<D>(sbase + (pair ? C::OFF_A2 : C::OFF_A1), pair ? g_a2 : g_a1, ta, pw, lane);
-            if (!KV && pair == 0) {  // the stationary queries' L and D
-                load_vec(sbase + C::OFF_VEC, p.nlse2, ta, pw, lane);
-                load_vec(sbase + C::OFF_VEC + 4 * kTileRows, p.delta, ta, pw, lane);
-            }
-            cp_async_arrive_noinc(bar(C::B_STAT));
-        }
+        cp_async_arrive_noinc(bar(C::B_STAT));
         bool ok = true;
         for (int j = 0; j < nstream; ++j) {
             const int s = j % ns;
