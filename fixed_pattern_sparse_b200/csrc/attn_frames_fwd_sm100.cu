@@ -941,17 +941,26 @@ bool frames_halves(const Geometry& g, long long n, long long keys) {
     return 10 * waves(kBM) * ((steps + 1) / 2 * (g.d == 128 ? 3 : 2) + 6) < 9 * waves(2 * kBM) * (2 * steps + 6);
 }
 
-// Splits of the key range: enough CTAs for one per SM (148) from a call with fewer, as long as
-// each part keeps at least four key tiles. The cache's capacity stands for its length, which
-// only the device knows.
+// Splits of the key range of a cache call: the number that ends first by waves of one CTA per SM (148)
+// times key tiles (five steps' worth of them for a CTA's start and end), where the fp32 partial results
+// cost a step per 5 MB, each part keeping at least four key tiles. (Measured: 96 CTAs of 168 tiles
+// 0.46 ms, cut into three 0.40; 640 of 151 tiles 1.75 ms, in two 1.88.) The cache's capacity stands for
+// its length, which only the device knows.
 int cached_splits(const Geometry& g, int cap) {
     if (cached_small(g)) return cached_small_splits(g, cap);
     const long long n = static_cast<long long>(g.T) * max_class_tokens(g), keys = static_cast<long long>(cap) * max_class_tokens(g);
-    const long long rows = frames_halves(g, n, keys) ? kBM : 2 * kBM;
-    const long long ctas = (n + rows - 1) / rows * g.heads * g.B * g.Ph * g.Pw, tiles = (keys + kBN - 1) / kBN;
-    long long s = 148 / ctas;
-    if (s > tiles / 4) s = tiles / 4;
-    return static_cast<int>(s < 1 ? 1 : s);
+    const long long rows = frames_halves(g, n, keys) ? kBM : 2 * kBM, pairs = static_cast<long long>(g.heads) * g.B * g.Ph * g.Pw;
+    const long long ctas = (n + rows - 1) / rows * pairs, tiles = (keys + kBN - 1) / kBN;
+    long long best = 1, least = -1;
+    for (long long s = 1; s <= 148 && (s == 1 || s * 4 <= tiles); ++s) {
+        const long long cost = (ctas * s + 147) / 148 * ((tiles + s - 1) / s + (rows == kBM ? 10 : 5)) +
+                               (s > 1 ? 2 + n * pairs * s * g.d * 8 / 5000000 : 0);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return static_cast<int>(best);
 }
 
 int launch_frames_fwd(FramesFwdParams p, const Geometry& g, void* stream) {
