@@ -23,7 +23,7 @@
 // of HBM delivers its 4 KB.
 // Key groups are dealt to the warps of a CTA and, over long caches, to `splits` CTAs; warps join
 // through shared memory, CTAs through the join kernel of attn_frames_fwd_sm100.cu. A CTA has
-// 8, 16 or 32 queries.
+// 8, 16, 24 or 32 queries.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -55,7 +55,7 @@ struct SmallCfg {
     static constexpr int VB = D / 8;                  // bytes of a lane's copy of a value
     static constexpr int KSTEPS = D / 16;
     static constexpr int MT = D / 16;                 // row tiles of O^T
-    static constexpr int CTAS = NQ == 4 ? 2 : NQ == 2 ? 3 : 4;  // per SM, by registers
+    static constexpr int CTAS = NQ == 4 ? 2 : NQ == 1 ? 4 : 3;  // per SM, by registers
 };
 
 template <int BYTES>
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
 }
 
 // Tiles of 8 queries of a CTA for classes of n queries.
-int query_tiles(long long n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
+int query_tiles(long long n) { return n >= 32 ? 4 : static_cast<int>((n + 7) / 8); }
 
 template <int D, int NQ>
 int launch_small_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
@@ -450,6 +450,7 @@ int launch_small(const FramesFwdParams& p, const Geometry& g, cudaStream_t strea
     switch (query_tiles(static_cast<long long>(g.T) * max_class_tokens(g))) {
         case 1: return launch_small_d<D, 1>(p, g, stream);
         case 2: return launch_small_d<D, 2>(p, g, stream);
+        case 3: return launch_small_d<D, 3>(p, g, stream);
         default: return launch_small_d<D, 4>(p, g, stream);
     }
 }
@@ -458,14 +459,14 @@ int launch_small(const FramesFwdParams& p, const Geometry& g, cudaStream_t strea
 
 bool cached_small(const Geometry& g) { return static_cast<long long>(g.T) * max_class_tokens(g) <= kMaxRows; }
 
-// One wave of CTAs for up to 16 queries a class, two for up to 32, of at least 512 keys each (measured:
+// One wave of CTAs for up to 24 queries a class, two for more, of at least 512 keys each (measured:
 // more CTAs cost up to a quarter in small calls and gain nothing in large ones).
 int cached_small_splits(const Geometry& g, int cap) {
     const long long n = static_cast<long long>(g.T) * max_class_tokens(g);
     const int tiles = query_tiles(n), rows = 8 * tiles;
     const long long keys = static_cast<long long>(cap) * max_class_tokens(g);
     const long long ctas = (n + rows - 1) / rows * g.heads * g.B * g.Ph * g.Pw;
-    long long s = 148LL * (tiles == 2 ? 3 : 4) / ctas;
+    long long s = 148LL * (tiles == 2 || tiles == 3 ? 3 : 4) / ctas;
     if (s > keys / 512) s = keys / 512;
     return static_cast<int>(s < 1 ? 1 : s);
 }
