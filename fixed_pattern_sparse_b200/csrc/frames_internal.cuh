@@ -134,12 +134,16 @@ inline int max_class_tokens(const Geometry& g) {  // tokens of one frame in the 
 
 inline void fill_frame_geom(FrameGeom& f, const Geometry& g) {
     f.T = g.T; f.H = g.H; f.W = g.W; f.heads = g.heads; f.Ph = g.Ph; f.Pw = g.Pw; f.mode = g.mode;
-    for (int c = 0; c < kMaxAxisClasses; ++c) {
+    for (int c = 0; c < g.Ph; ++c) {
         f.Rc[c] = g.Rc[c];
-        f.Sc[c] = g.Sc[c];
         f.dR[c].init(g.Rc[c]);
+    }
+    for (int c = 0; c < g.Pw; ++c) {
+        f.Sc[c] = g.Sc[c];
         f.dS[c].init(g.Sc[c]);
-        const int nF = c < g.Ph * g.Pw ? g.Rc[c / g.Pw] * g.Sc[c % g.Pw] : 0;
+    }
+    for (int c = 0; c < g.Ph * g.Pw; ++c) {
+        const int nF = g.Rc[c / g.Pw] * g.Sc[c % g.Pw];
         f.dF[c].init(nF);
         f.dC[c].init((nF + 31) / 32);
     }

@@ -90,8 +90,8 @@ def _size_of(name: str, *args) -> int:
 
 
 def _need(name: str, t, dtype, shape=None, device: int | None = None) -> None:
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
-            and (shape is None or t.shape == shape) and (device is None or t.get_device() == device)):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)
+            and (t.get_device() == device if device is not None else t.is_cuda)):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
@@ -124,14 +124,22 @@ def _bias(table, buckets, heads: int, device: int):
     return table.data_ptr(), buckets.data_ptr(), table.shape[0], n // 2
 
 
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same pointer without a Stream object, several microseconds of a small call, where torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _on(device: int, stream, call):
     """Runs call(stream pointer) with the tensors' device and the stream to work on current, so that
     what it allocates belongs to that stream."""
     if stream is None and device == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(_current_stream(device))
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_current_stream(device))
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
 
@@ -152,7 +160,7 @@ def _relbias_fwd(dims, q, k, v, table, buckets, P, mode, out, lse, out_lo, strea
 
     def call(st):
         o = torch.empty_like(q) if out is None else out
-        l = torch.empty(shape[:5], dtype=torch.float32, device=q.device) if lse is None else lse
+        l = q.new_empty(shape[:5], dtype=torch.float32) if lse is None else lse
         check(_entry(name, dims)(q.data_ptr(), k.data_ptr(), v.data_ptr(), *bias, o.data_ptr(),
                                  None if out_lo is None else out_lo.data_ptr(), l.data_ptr(), *shape, P, mode, st), name)
         return o, l
@@ -183,7 +191,7 @@ def _relbias_bwd(dims, q, k, v, out, dout, lse, table, buckets, P, mode, dq, dk,
     def call(st):
         grads = [torch.empty_like(q) if g is None else g for g in (dq, dk, dv)]
         grads.append(torch.empty_like(table) if dtable is None else dtable)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+        ws = q.new_empty(need, dtype=torch.uint8) if workspace is None else workspace
         check(_entry(name, dims)(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                  None if out_lo is None else out_lo.data_ptr(), dout.data_ptr(), lse.data_ptr(), *bias,
                                  *(g.data_ptr() for g in grads), ws.data_ptr(), ws.numel(), *shape, P, mode, st), name)
@@ -308,7 +316,7 @@ def _attn_cached(dims, q, cache, start, P, mode, table, buckets, out, lse, works
         o = torch.empty_like(q) if out is None else out
         ws = workspace
         if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = q.new_empty(need, dtype=torch.uint8)
         check(_entry(name, dims)(q.data_ptr(), *(t.data_ptr() for t in cache), start.data_ptr(), *bias, o.data_ptr(),
                                  None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
                                  0 if ws is None else ws.numel(), *shape, P, mode, capacity, st), name)
