@@ -633,7 +633,12 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                         ptx::tmem_wait_ld();
                         if (next >= 32) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, off));
+                            for (int e = 0; e < 32; e += 2) {  // two columns per instruction
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                                            make_float2(sl2, sl2), make_float2(off, off));
+                                sv[e] = __float_as_uint(y.x);
+                                sv[e + 1] = __float_as_uint(y.y);
+                            }
                         } else {
                             const float o1 = bias_of(++f);
 #pragma unroll
@@ -711,22 +716,26 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             // S, in two halves released as they are stored. A row that has seen no key yet keeps
             // the reference 0, so that its -inf scores give 0.
             const float neg = off - (m_run == -INFINITY ? 0.f : m_run) + (CACHE ? kPShift : 0.f);
-            float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;  // four short addition chains
+            float2 sum_a = make_float2(0.f, 0.f), sum_b = sum_a;  // four short addition chains
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float x0 = fmaf(sc[32 * g + 2 * e], mul, neg);
-                    const float x1 = fmaf(sc[32 * g + 2 * e + 1], mul, neg);
-                    const float p0 = ptx::ex2_approx(x0);
-                    const float p1 = ptx::ex2_approx(x1);
-                    if (e & 1) {
-                        sum2 += p0;
-                        sum3 += p1;
+                    // two columns per instruction (packed f32x2)
+                    const float2 x = __ffma2_rn(make_float2(sc[32 * g + 2 * e], sc[32 * g + 2 * e + 1]),
+                                                make_float2(mul, mul), make_float2(neg, neg));
+                    const float p0 = ptx::ex2_approx(x.x);
+                    const float p1 = ptx::ex2_approx(x.y);
+                    if (CACHE) {  // packed sums: 3 % faster here, 1 % slower in the bf16 form
+                        float2& sum = e & 1 ? sum_b : sum_a;
+                        sum = __fadd2_rn(sum, make_float2(p0, p1));
+                    } else if (e & 1) {
+                        sum_b.x += p0;
+                        sum_b.y += p1;
                     } else {
-                        sum0 += p0;
-                        sum1 += p1;
+                        sum_a.x += p0;
+                        sum_a.y += p1;
                     }
                     pk[e] = CACHE ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
                 }
@@ -753,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + (g >> 1)));
                 }
             }
-            l_run = l_run * alpha + ((sum0 + sum1) + (sum2 + sum3));
+            l_run = l_run * alpha + ((sum_a.x + sum_a.y) + (sum_b.x + sum_b.y));
         }
         if (ok && (nkv == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_OFULL), 0, abort, lim)))) {
             ptx::tc_fence_after();
