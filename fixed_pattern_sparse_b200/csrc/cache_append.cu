@@ -28,7 +28,7 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) skiparse_cache_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 8) skiparse_cache_append_kernel(const AppendParams p) {
     constexpr int CPR = D / 8;                       // 16-byte chunks of a row
     constexpr int PER = kCacheBlock * CPR / kThreads;  // chunks of a thread (1, 2, 4)
     static_assert(PER >= 1, "block too small");

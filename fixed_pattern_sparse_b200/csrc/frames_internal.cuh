@@ -29,7 +29,7 @@ struct FrameBias {
 struct FrameGeom {
     int T, H, W, heads, Ph, Pw, mode;
     int Rc[kMaxAxisClasses], Sc[kMaxAxisClasses];
-    FastDiv dR[kMaxAxisClasses], dS[kMaxAxisClasses], dF[kMaxAxisClasses], dC[kMaxAxisClasses], dPh, dPw;
+    FastDiv dR[kMaxAxisClasses], dS[kMaxAxisClasses], dF[kMaxAxisClasses], dC[kMaxAxisClasses], dPh, dPw, dClasses;
 };
 
 // The e4m3 frame cache of one layer: codes (B*classes, heads, cap, F, d), F the padded tokens
@@ -149,6 +149,7 @@ inline void fill_frame_geom(FrameGeom& f, const Geometry& g) {
     }
     f.dPh.init(g.Ph);
     f.dPw.init(g.Pw);
+    f.dClasses.init(g.Ph * g.Pw);
 }
 
 // One (batch, class, head) of a call: its sizes and row map.
@@ -156,10 +157,9 @@ struct ClassView {
     int b, c, ci, cj, Rc, Sc, nF;  // nF: tokens per frame
     FastDiv dF;
     __device__ __forceinline__ void init(const FrameGeom& g, int seq) {
-        const int q2 = g.Ph * g.Pw;
-        b = seq / q2;
-        c = seq - b * q2;
-        ci = c / g.Pw;
+        b = g.dClasses.div(seq);
+        c = seq - b * g.Ph * g.Pw;
+        ci = g.dPw.div(c);
         cj = c - ci * g.Pw;
         Rc = g.Rc[ci];
         Sc = g.Sc[cj];
