@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
     int f_lo, f_hi;
     ring.visible(start + dF.div(q_first), start + dF.div(min(q_first + C::ROWS, n_q) - 1), range[0], range[1], dmax, f_lo, f_hi);
     const int groups = f_hi >= f_lo ? ((f_hi - f_lo + 1) * nF + kKeys - 1) / kKeys : 0;
-    const int per_split = (groups + p.splits - 1) / p.splits;
+    const int per_split = (groups + p.plan.splits - 1) / p.plan.splits;
     const int jend = (f_hi + 1) * nF;
     const int jbeg = f_lo * nF + split * per_split * kKeys;
     const int mygroups = max(0, min(per_split, groups - split * per_split));
@@ -409,11 +409,11 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
         const float l2 = total == 0.f ? -INFINITY : top + ptx::lg2_approx(total);
         const long long grow = rows(qi);
         if (!row_ok(grow, p.nrows, p.status)) continue;
-        if (p.splits > 1) {
-            float* dst = p.part_o + (grow * p.splits + split) * D + lane * PER;
+        if (p.plan.splits > 1) {
+            float* dst = p.part_o + (grow * p.plan.splits + split) * D + lane * PER;
 #pragma unroll
             for (int e = 0; e < PER; ++e) dst[e] = acc[e] * scale;
-            if (lane == 0) p.part_l[grow * p.splits + split] = l2;
+            if (lane == 0) p.part_l[grow * p.plan.splits + split] = l2;
         } else {
             uint16_t* dst = p.out + grow * D + lane * PER;
 #pragma unroll
@@ -440,7 +440,7 @@ int launch_small_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t str
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
     const int row_tiles = (g.T * max_class_tokens(g) + C::ROWS - 1) / C::ROWS;
-    const dim3 grid(static_cast<unsigned>(row_tiles) * p.splits, g.heads, g.B * g.Ph * g.Pw);
+    const dim3 grid(static_cast<unsigned>(row_tiles) * p.plan.splits, g.heads, g.B * g.Ph * g.Pw);
     skiparse_cached_small_kernel<D, NQ><<<grid, 32 * kWarps, C::SMEM_BYTES, stream>>>(p, row_tiles);
     return static_cast<int>(cudaGetLastError());
 }

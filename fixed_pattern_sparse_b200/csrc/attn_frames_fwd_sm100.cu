@@ -24,9 +24,9 @@
 //     the largest scale, and within 2^-34 of the largest magnitude below. Q's rows are scaled by a
 //     power of two each into f16, and P is kept as 2^7 p, so that f16 holds every p above 2^-31:
 //     P's rounding is 2^-11 instead of bf16's 2^-8.
-//   * Few query tiles over a long cache leave SMs idle: the key range is then cut into `splits`
-//     parts, each CTA writes its normalised partial output and log-sum-exp in fp32, and
-//     a second kernel joins them.
+//   * Few query tiles over a long cache leave SMs idle, and so does a last wave of few CTAs: the key
+//     range of these tiles is cut into parts, each CTA writes its normalised partial output and
+//     log-sum-exp in fp32, and a second kernel joins them.
 //   * Calls of few query tiles: a CTA may own 128 queries instead, its two softmax groups taking
 //     every other key tile each (an own O in TMEM each, joined at the end), which halves the
 //     length of a CTA and doubles their number.
@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "frames_common.cuh"
 
@@ -266,11 +267,18 @@ __device__ __forceinline__ int q_row_to_f16(uint32_t tile, int row) {
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frames_kernel(const FramesFwdParams p) {
     using C = Cfg<D, CACHE>;
-    const int npairs = gridDim.x / p.splits;
-    const int split = blockIdx.x % p.splits;
-    const int pair = npairs - 1 - blockIdx.x / p.splits;
-    const int head = blockIdx.y;
-    const int seq = blockIdx.z;
+    int pair = p.npairs - 1 - blockIdx.x, head = blockIdx.y, seq = blockIdx.z;
+    // cache: this CTA's number among those of the items that are cut, negative for a whole item
+    const int over = CACHE ? static_cast<int>(blockIdx.x) - static_cast<int>(p.plan.whole) : -1;
+    const int splits = over >= 0 ? p.plan.splits : 1;
+    if (CACHE) {
+        const int item = blockIdx.x - (over >= 0 ? over - p.dSplits.div(over) : 0);
+        seq = p.dPairs.div(item);
+        pair = p.npairs - 1 - (item - seq * p.npairs);
+        head = seq;
+        seq = p.dHeads.div(seq);
+        head -= seq * p.g.heads;
+    }
     ClassView cls;
     cls.init(p.g, seq);
     const int nF = cls.nF;
@@ -366,10 +374,11 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     int f_lo, f_hi;  // frames that some row of this CTA can see
     ring.visible(start + dF.div(q_first), start + dF.div(min(q_first + (halves ? kBM : 2 * kBM), n_q) - 1), dlo, dhi, dmax, f_lo, f_hi);
     const int nkv_all = f_hi >= f_lo ? ((f_hi - f_lo + 1) * nF + kBN - 1) / kBN : 0;
-    const int per_split = (nkv_all + p.splits - 1) / p.splits;
+    const int per_split = (nkv_all + splits - 1) / splits;
     const int jend = (f_hi + 1) * nF;                          // end of the visible keys
-    const int jbeg = f_lo * nF + split * per_split * kBN;      // this CTA's first key
-    const int nkv = max(0, min(per_split, nkv_all - split * per_split));
+    const int first_tile = over >= 0 ? (over - p.dSplits.div(over) * splits) * per_split : 0;
+    const int jbeg = f_lo * nF + first_tile * kBN;             // this CTA's first key
+    const int nkv = max(0, min(per_split, nkv_all - first_tile));
     // cache: the largest scale among the keys read. Codes enter the tensor core as f16 values
     // code * 2^(e - ref), so that one power of two for K and one for V remain to be applied.
     const long long sh = static_cast<long long>(seq) * p.g.heads + head;
@@ -794,9 +803,15 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             }
             const bool real = qi < n_q && !(halves && qt == 1) && row_ok(rows(qi), p.nrows, p.status);
             const size_t grow = real ? static_cast<size_t>(rows(qi)) : 0;
+            const bool partial = CACHE && splits > 1;
+            size_t part = 0;  // its place
+            if (partial) {
+                const int cut = p.dSplits.div(over);
+                part = (static_cast<size_t>(cut) * (p.halves ? kBM : 2 * kBM) + (qi - q_first)) * splits + (over - cut * splits);
+            }
             if (real) {
-                if (p.splits > 1)
-                    p.part_l[grow * p.splits + split] = l2;
+                if (partial)
+                    p.part_l[part] = l2;
                 else if (p.lse)
                     p.lse[grow] = l2 * 0.6931471805599453f;
             }
@@ -816,9 +831,9 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                         ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), inv_l, join * other[(32 * g + e) * kBM]));
                 }
                 const float inv = halves && nkv > 1 ? 1.f : inv_l;
-                if (p.splits > 1) {
+                if (partial) {
                     if (real) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + (grow * p.splits + split) * D + 32 * g);
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * g);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
@@ -863,24 +878,39 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
 // w_s = 2^(l_s - max l). One warp per query row.
 template <int D>
 __global__ void __launch_bounds__(256) skiparse_frames_join_kernel(const FramesFwdParams p) {
-    const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const long long at = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;  // partial results' row
     const int lane = threadIdx.x & 31;
-    if (row >= p.nrows) return;
-    const long long per_b = static_cast<long long>(p.g.T) * p.g.H * p.g.W * p.g.heads;
-    const int start = p.cache.start[row / per_b];
-    if (start < 0 || start > kMaxStart) return;
-    const float* l = p.part_l + row * p.splits;
+    if (at >= p.plan.part_rows) return;
+    const int splits = p.plan.splits;
+    long long row = at;
+    int b;
+    if (p.npairs == 0) {  // few-query form
+        b = static_cast<int>(row / (static_cast<long long>(p.g.T) * p.g.H * p.g.W * p.g.heads));
+    } else {
+        const int per = p.halves ? kBM : 2 * kBM;
+        const int item = static_cast<int>(p.plan.whole) + static_cast<int>(at / per);
+        const int sh = p.dPairs.div(item), seq = p.dHeads.div(sh);
+        const int qi = (p.npairs - 1 - (item - sh * p.npairs)) * per + static_cast<int>(at % per);
+        ClassView cls;
+        cls.init(p.g, seq);
+        if (qi >= p.g.T * cls.nF) return;
+        row = cls.rows(p.g, sh - seq * p.g.heads)(qi);
+        b = cls.b;
+    }
+    const int start = p.cache.start[b];
+    if (start < 0 || start > kMaxStart || !row_ok(row, p.nrows, p.status)) return;
+    const float* l = p.part_l + at * splits;
     float m = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, l[s]);
+    for (int s = lane; s < splits; s += 32) m = fmaxf(m, l[s]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     constexpr int PER = D / 32;
     float acc[PER] = {}, total = 0.f;
     m = m == -INFINITY ? 0.f : m;  // no key seen, or NaNs alone, which have to stay
-    for (int s = 0; s < p.splits; ++s) {
+    for (int s = 0; s < splits; ++s) {
         const float w = ptx::ex2_approx(l[s] - m);
         total += w;
-        const float* o = p.part_o + (row * p.splits + s) * D + lane * PER;
+        const float* o = p.part_o + (at * splits + s) * D + lane * PER;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
     }
@@ -892,7 +922,7 @@ __global__ void __launch_bounds__(256) skiparse_frames_join_kernel(const FramesF
 }
 
 int launch_frames_join(const FramesFwdParams& p, int d, cudaStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>((p.nrows + 7) / 8);
+    const unsigned blocks = static_cast<unsigned>((p.plan.part_rows + 7) / 8);
     switch (d) {
         case 32: skiparse_frames_join_kernel<32><<<blocks, 256, 0, stream>>>(p); break;
         case 64: skiparse_frames_join_kernel<64><<<blocks, 256, 0, stream>>>(p); break;
@@ -922,12 +952,14 @@ int launch_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
         }
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
-    const long long n_max = static_cast<long long>(g.T) * max_class_tokens(g);
-    const int rows = p.halves ? kBM : 2 * kBM;
-    const dim3 grid(static_cast<unsigned>((n_max + rows - 1) / rows * p.splits), g.heads, g.B * g.Ph * g.Pw);
+    dim3 grid(p.npairs, g.heads, g.B * g.Ph * g.Pw);
+    if (CACHE) {
+        const long long items = static_cast<long long>(grid.x) * grid.y * grid.z;
+        grid = dim3(static_cast<unsigned>(p.plan.whole + (items - p.plan.whole) * p.plan.splits));
+    }
     skiparse_attn_frames_kernel<D, CACHE><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return static_cast<int>(e);
+    if (e != cudaSuccess || !CACHE || p.plan.splits == 1) return static_cast<int>(e);
     return launch_frames_join(p, D, stream);
 }
 
@@ -950,26 +982,29 @@ bool frames_halves(const Geometry& g, long long n, long long keys) {
     return 10 * waves(kBM) * ((steps + 1) / 2 * (g.d == 128 ? 3 : 2) + 6) < 9 * waves(2 * kBM) * (2 * steps + 6);
 }
 
-// Splits of the key range of a cache call: the number that ends first by waves of one CTA per SM (148)
-// times key tiles (five steps' worth of them for a CTA's start and end), where the fp32 partial results
-// cost a step per 5 MB, each part keeping at least four key tiles. (Measured: 96 CTAs of 168 tiles
-// 0.46 ms, cut into three 0.40; 640 of 151 tiles 1.75 ms, in two 1.88.) The cache's capacity stands for
-// its length, which only the device knows.
-int cached_splits(const Geometry& g, int cap) {
-    if (cached_small(g)) return cached_small_splits(g, cap);
+// How a cache call is cut: the choice that ends first by waves of one CTA per SM (148) times key tiles
+// (five steps' worth of them for a CTA's start and end), where the fp32 partial results cost a step per
+// 5 MB, each part keeping at least four key tiles. Either every item is cut (96 items of 168 tiles took
+// 0.46 ms, in three parts each 0.40), or those behind the last full wave (640 items of 151 tiles: 1.57 ms
+// whole, 1.45 with the last 48 in three parts; 480 of 75: 0.73 and 0.65). The cache's capacity stands for its length, which only the device knows.
+CachePlan cached_plan(const Geometry& g, int cap) {
     const long long n = static_cast<long long>(g.T) * max_class_tokens(g), keys = static_cast<long long>(cap) * max_class_tokens(g);
-    const long long rows = frames_halves(g, n, keys) ? kBM : 2 * kBM, pairs = static_cast<long long>(g.heads) * g.B * g.Ph * g.Pw;
-    const long long ctas = (n + rows - 1) / rows * pairs, tiles = (keys + kBN - 1) / kBN;
-    long long best = 1, least = -1;
-    for (long long s = 1; s <= 148 && (s == 1 || s * 4 <= tiles); ++s) {
-        const long long cost = (ctas * s + 147) / 148 * ((tiles + s - 1) / s + (rows == kBM ? 10 : 5)) +
-                               (s > 1 ? 2 + n * pairs * s * g.d * 8 / 5000000 : 0);
-        if (least < 0 || cost < least) {
+    const long long pairs = static_cast<long long>(g.heads) * g.B * g.Ph * g.Pw;
+    if (cached_small(g)) return {0, cached_small_splits(g, cap), static_cast<long long>(g.B) * g.T * g.H * g.W * g.heads};
+    const long long rows = frames_halves(g, n, keys) ? kBM : 2 * kBM, tiles = (keys + kBN - 1) / kBN;
+    const long long items = (n + rows - 1) / rows * pairs, ends = rows == kBM ? 10 : 5;
+    CachePlan best{items, 1, 0};
+    long long least = -1;
+    for (const long long whole : {items / 148 * 148, 0ll})
+        for (long long s = 1; s <= 148 && (s == 1 || s * 4 <= tiles); ++s) {
+            const long long cut = items - whole, part_rows = s > 1 ? cut * rows : 0;
+            const long long cost = whole / 148 * (tiles + ends) + (cut * s + 147) / 148 * ((tiles + s - 1) / s + ends) +
+                                   (s > 1 ? 2 + part_rows * s * g.d * 8 / 5000000 : 0);
+            if (least >= 0 && cost >= least) continue;
             least = cost;
-            best = s;
+            best = {s > 1 ? whole : items, static_cast<int>(s), part_rows};
         }
-    }
-    return static_cast<int>(best);
+    return best;
 }
 
 int launch_frames_fwd(FramesFwdParams p, const Geometry& g, void* stream) {
@@ -978,8 +1013,14 @@ int launch_frames_fwd(FramesFwdParams p, const Geometry& g, void* stream) {
                              static_cast<long long>(p.cache.k ? p.cache.cap : g.T) * max_class_tokens(g));
     if (p.cache.k && cached_small(g)) {
         const int e = launch_cached_small(p, g, stream);
-        return e || p.splits == 1 ? e : launch_frames_join(p, g.d, st);
+        return e || p.plan.splits == 1 ? e : launch_frames_join(p, g.d, st);
     }
+    const long long n_max = static_cast<long long>(g.T) * max_class_tokens(g);
+    const int rows = p.halves ? kBM : 2 * kBM;
+    p.npairs = static_cast<int>((n_max + rows - 1) / rows);
+    p.dPairs.init(p.npairs);
+    p.dHeads.init(g.heads);
+    p.dSplits.init(p.plan.splits);
     switch (g.d) {
         case 32: return launch_kind<32>(p, g, st);
         case 64: return launch_kind<64>(p, g, st);

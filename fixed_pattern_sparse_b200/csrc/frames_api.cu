@@ -79,7 +79,6 @@ int relbias_fwd(int dims, const void* q, const void* k, const void* v, const voi
     if (!(p.status = api::status_word())) return SKIPARSE_ERR_CUDA;
     skiparse::fill_frame_geom(p.g, g);
     p.bias = make_bias(table, buckets, num_buckets, max_distance);
-    p.splits = 1;
     p.scale_log2 = static_cast<float>(log2e_over_sqrt(d));
     p.wait_limit_ns = api::wait_limit_ns();
     p.fault = api::pending_fault(1);
@@ -241,17 +240,17 @@ int cache_append(int dims, const void* k, const void* v, const int* start, void*
     return e == 0 ? SKIPARSE_OK : api::cuda_fail(e);
 }
 
-size_t cached_space(const Geometry& g, int capacity) {
-    const size_t splits = skiparse::cached_splits(g, capacity);
-    const size_t rows = static_cast<size_t>(g.B) * g.T * g.H * g.W * g.heads;
-    return splits == 1 ? 0 : pad256(rows * splits * 4) + rows * splits * g.d * 4;
+// Workspace of a cache call: log-sum-exps, then outputs, of the parts of its split items.
+size_t cached_part_l(const skiparse::CachePlan& c) { return pad256(static_cast<size_t>(c.part_rows) * c.splits * 4); }
+size_t cached_space(const skiparse::CachePlan& c, int d) {
+    return c.splits == 1 ? 0 : cached_part_l(c) + static_cast<size_t>(c.part_rows) * c.splits * d * 4;
 }
 
 long long cached_workspace(int dims, int B, int T, int H, int W, int heads, int d, int P, int capacity) {
     Geometry g, h;
     if (cache_geometry(dims, B, T, H, W, heads, d, P, SKIPARSE_TOKEN_WISE, capacity, g) != SKIPARSE_OK) return -1;
     cache_geometry(dims, B, T, H, W, heads, d, P, SKIPARSE_GROUP_WISE, capacity, h);
-    const size_t a = cached_space(g, capacity), b = cached_space(h, capacity);
+    const size_t a = cached_space(skiparse::cached_plan(g, capacity), d), b = cached_space(skiparse::cached_plan(h, capacity), d);
     return static_cast<long long>(a > b ? a : b);
 }
 
@@ -269,7 +268,8 @@ int attn_cached(int dims, const void* q, const void* k_cache, const void* v_cach
         if (!aligned(ptr, 16)) return SKIPARSE_ERR_MISALIGNED;
     if (!aligned(start, 4) || (lse && !aligned(lse, 4)) || (workspace && !aligned(workspace, 256)))
         return SKIPARSE_ERR_MISALIGNED;
-    const size_t need = cached_space(g, capacity);
+    const skiparse::CachePlan plan = skiparse::cached_plan(g, capacity);
+    const size_t need = cached_space(plan, d);
     if (need && (!workspace || workspace_bytes < need)) return SKIPARSE_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(B) * T * H * W * heads;
     const size_t tb = static_cast<size_t>(rows) * d * 2;
@@ -283,9 +283,9 @@ int attn_cached(int dims, const void* q, const void* k_cache, const void* v_cach
     p.q = static_cast<const uint16_t*>(q);
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
-    p.splits = skiparse::cached_splits(g, capacity);
+    p.plan = plan;
     p.part_l = static_cast<float*>(workspace);
-    p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pad256(static_cast<size_t>(rows) * p.splits * 4));
+    p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + cached_part_l(plan));
     if (!(p.status = api::status_word())) return SKIPARSE_ERR_CUDA;
     skiparse::fill_frame_geom(p.g, g);
     p.bias = make_bias(table, buckets, num_buckets, max_distance);

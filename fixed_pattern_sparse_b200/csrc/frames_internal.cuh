@@ -48,6 +48,16 @@ struct CacheView {
     int cap, F, NBk;
 };
 
+// How a cache call is cut into CTAs. An item is a tile of queries of one class and head. The first
+// `whole` items are a CTA each; of the others, the keys are cut into `splits` parts, a CTA each, whose
+// results a second kernel joins.
+struct CachePlan {
+    long long whole;
+    int splits;
+    long long part_rows;  // rows with partial results: those of the items that are cut; every row of the call, in
+                          // its order, in the few-query form (which has no whole items)
+};
+
 // Forward: bf16 keys and values (k, v), or the cache (cache.k != nullptr).
 struct FramesFwdParams {
     const uint16_t* q;
@@ -56,14 +66,16 @@ struct FramesFwdParams {
     uint16_t* out;
     uint16_t* out_lo; // optional: out's rounding residual (bf16 keys only)
     float* lse;       // optional
-    float* part_o;    // splits > 1: (rows, splits, d) fp32 normalised partial outputs
-    float* part_l;    // splits > 1: (rows, splits) fp32 partial log2-sum-exp
+    float* part_o;    // splits > 1: (part_rows, splits, d) fp32 normalised partial outputs
+    float* part_l;    // splits > 1: (part_rows, splits) fp32 partial log2-sum-exp
     int* status;
     FrameGeom g;
     FrameBias bias;
     CacheView cache;
-    int splits;
+    CachePlan plan;   // cache only
     int halves;       // 128-query CTAs; chosen by launch_frames_fwd
+    int npairs;       // query tiles of the longest class; this and the divisions: set by launch_frames_fwd
+    FastDiv dPairs, dHeads, dSplits;
     float scale_log2;
     unsigned long long wait_limit_ns;
     int fault;
@@ -119,9 +131,9 @@ int launch_cache_append(const AppendParams& p, const Geometry& g, int d, void* s
 bool cached_small(const Geometry& g);
 int cached_small_splits(const Geometry& g, int cap);
 int launch_cached_small(const FramesFwdParams& p, const Geometry& g, void* stream);
-// Key splits that launch_frames_fwd should be given for a cache call of these sizes (1: no
+// The plan that launch_frames_fwd should be given for a cache call of these sizes (splits 1: no
 // workspace is needed).
-int cached_splits(const Geometry& g, int cap);
+CachePlan cached_plan(const Geometry& g, int cap);
 
 inline int max_class_tokens(const Geometry& g) {  // tokens of one frame in the largest class
     int r = 0, s = 0;

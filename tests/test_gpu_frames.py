@@ -372,6 +372,33 @@ def test_skipped_sequences_are_left_alone(fps, cap, T, shape):
     check("out", out[:1], want[:1], tol[:1])
 
 
+@pytest.mark.parametrize("d,cap,start", [(32, 9, [8, 30, 4]), (64, 9, [8, 30, -1]), (128, 9, [3, -1, 20])])
+def test_last_wave_is_cut(fps, d, cap, start):
+    """More query tiles than one wave: the keys of the tiles behind the last full wave, those of the last
+    sequence, are cut into parts and joined."""
+    shape, P, mode = (3, 1, 29, 41, 13, d), 2, 0
+    B, T, H, W, h, _ = shape
+    need = fps._lib.lib().skiparse2d_attn_cached_workspace_bytes(*shape, P, cap)
+    assert 0 < need < B * T * H * W * h * d * 4  # parts of some rows only
+    cache = fps.frame_cache(B, cap, H, W, h, d, P)
+    fill = torch.zeros(B, dtype=torch.int32, device="cuda")
+    fps.skiparse2d_cache_append(normal((B, cap, H, W, h, d), 41), normal((B, cap, H, W, h, d), 42), fill, cache, P, mode)
+    first = torch.tensor(start, dtype=torch.int32, device="cuda")
+    fps.skiparse2d_cache_append(normal(shape, 43), normal(shape, 44), first, cache, P, mode)
+    q, table, buckets = normal(shape, 45), normal((9, h), 46, 0.7), fps.frame_buckets(12, 9, causal=True)
+    out, lse = torch.full_like(q, 7.0), torch.full(shape[:5], 7.0, device="cuda")
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    fps.skiparse2d_attn_cached(q, cache, first, P, mode, table=table, buckets=buckets, out=out, lse=lse, workspace=ws)
+    assert fps.get_device_status() == 0
+    want, tol, want_lse = cached_reference(q, cache, start, P, mode, table, buckets)
+    for b in range(B):
+        if start[b] < 0:
+            assert (out[b] == 7).all() and (lse[b] == 7).all()
+        else:
+            check("out", out[b], want[b], tol[b])
+            check("lse", lse[b], want_lse[b], torch.full_like(want_lse[b], 1e-4))
+
+
 def test_a_row_without_visible_keys(fps):
     """A map that shows only frames further back than the cache holds."""
     for cap, shape in ((3, (1, 1, 8, 8, 2, 64)), (600, (1, 1, 2, 2, 2, 64))):
