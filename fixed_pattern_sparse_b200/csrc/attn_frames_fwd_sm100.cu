@@ -49,6 +49,79 @@ constexpr int kMaxSmem = 232448;      // 227 KB, the most a CTA may have
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by more than 2^8
 constexpr int kPParts = 2;            // P is released to the tensor core in two halves of the key tile
 
+// The bias as part of S = Q K^T (bf16 keys): 16 more columns of Q and K. The frames of a CTA's queries, at
+// most five, are numbered; a query's row holds ones in the three columns of its frame, a key's row holds,
+// for each of these frames, its bias for that frame's queries in units of q.k as the sum of three bf16
+// numbers (24 bits), so that the tensor core adds it to each score in fp32. That replaces a pass over S in
+// TMEM for every tile that holds a frame's border; a CTA whose queries lie in more frames takes the pass.
+// A key's row depends on its distance from the first of the queries' frames only: these rows are made
+// once per CTA and copied. Taken by 256-query CTAs and frames of up to 8 d tokens: 390 tokens, d = 128:
+// 1.53 -> 1.44 ms, as fast as without a bias; 225, d = 64: 642 -> 598 us; 81, d = 32: 621 -> 511 us. Beyond,
+// borders are rare and the MMA step costs more than they do (1296, d = 128: 1.36 -> 1.37 ms; 900, d = 64:
+// 1.05 -> 1.09 ms), and in 128-query CTAs, which load twice the keys, so do the producers' copies (144
+// tokens, d = 128: 42.5 -> 45.5 us).
+struct BiasCols {
+    static constexpr int FRAMES = 5, ROW = 32, TILE_BYTES = kBN * ROW;
+    static constexpr uint32_t LAYOUT = 6;           // 32-byte swizzle
+    static constexpr int MAX_ROWS = kMaxDistEntries + FRAMES - 1;  // distances -D-4 .. D
+    // A masked pair: far below any score, and finite, since zeros multiply it for the other frames.
+    static constexpr float MASKED = -1.7014118346046923e38f;  // -2^127
+    // Scaled scores beyond +-FAR stand for masked keys, or for an entry of the table that is not finite.
+    static constexpr float FAR_LOG2 = 1e35f;
+
+    static __device__ __forceinline__ void store16(uint32_t at, const uint32_t (&w)[4]) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+    // Address of 16-byte half c of row r of a tile.
+    static __device__ __forceinline__ uint32_t half_at(uint32_t tile, int r, int c) {
+        return tile + r * ROW + ((c ^ ((r >> 2) & 1)) << 4);
+    }
+    // Row r of a query tile: ones for frame number fi.
+    static __device__ __forceinline__ void store_query(uint32_t tile, int r, int fi) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int lo = 8 * c + 2 * e - 3 * fi, hi = lo + 1;
+                w[e] = (lo >= 0 && lo < 3 ? 0x3f80u : 0u) | (hi >= 0 && hi < 3 ? 0x3f800000u : 0u);
+            }
+            store16(half_at(tile, r, c), w);
+        }
+    }
+    // The row, at `at`, of keys at distance u from the queries' first frame; tab: the bias by distance in log2.
+    static __device__ __forceinline__ void make_row(uint32_t at, const float* tab, int u, int dmax, float sl2) {
+        uint32_t t[16];
+#pragma unroll
+        for (int i = 0; i < FRAMES; ++i) {
+            const float l2 = tab[clamp_dist(u + i, dmax) + dmax];
+            float x = l2 == -INFINITY ? MASKED : fabsf(l2) < 1e37f ? l2 / sl2 : -MASKED;
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                t[3 * i + e] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                x -= __uint_as_float(t[3 * i + e] << 16);
+            }
+        }
+        t[15] = 0u;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t w[4] = {t[8 * c] | t[8 * c + 1] << 16, t[8 * c + 2] | t[8 * c + 3] << 16,
+                                   t[8 * c + 4] | t[8 * c + 5] << 16, t[8 * c + 6] | t[8 * c + 7] << 16};
+            store16(at + 16 * c, w);
+        }
+    }
+    // Row r of a key tile, for a key at distance u from the queries' first frame.
+    static __device__ __forceinline__ void store_key(uint32_t tile, int r, uint32_t rows, int u, int dmax) {
+        const uint32_t at = rows + (min(max(u, -dmax - FRAMES + 1), dmax) + dmax + FRAMES - 1) * ROW;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at + 16 * c));
+            store16(half_at(tile, r, c), w);
+        }
+    }
+};
+
 template <int D, bool CACHE>
 struct Cfg : TileGeom<D> {
     using G = TileGeom<D>;
@@ -65,7 +138,12 @@ struct Cfg : TileGeom<D> {
     static constexpr int OFF_K = 2 * TILE_BYTES;
     static constexpr int OFF_V = OFF_K + KST * TILE_BYTES;
     static constexpr int OFF_STAGE = OFF_V + VST * TILE_BYTES;  // cache: a tile of codes of K and of V
-    static constexpr int OFF_TAB = OFF_STAGE + (CACHE ? 2 * kBN * D : 0);  // bias by distance index
+    // bf16: the bias columns of the two query tiles and of the K ring's slots (see BiasCols)
+    static constexpr int OFF_QB = OFF_STAGE;
+    static constexpr int OFF_KB = OFF_QB + 2 * BiasCols::TILE_BYTES;
+    static constexpr int OFF_ROWS = OFF_KB + KST * BiasCols::TILE_BYTES;
+    static constexpr int OFF_TAB =                                // bias by distance index
+        CACHE ? OFF_STAGE + 2 * kBN * D : OFF_ROWS + BiasCols::MAX_ROWS * BiasCols::ROW;
     static constexpr int OFF_BAR = OFF_TAB + 4 * (kMaxDistEntries + 1);
     static constexpr int B_Q = 0;
     static constexpr int B_KFULL = 1;
@@ -320,10 +398,15 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int dmax = p.bias.D;
     const RowMap rows = cls.rows(p.g, head);
 
+    // bf16: the frames of this CTA's queries, and whether the bias comes with the scores
+    const int q_frame = dF.div(q_first);
+    const int q_frames = dF.div(min(q_first + (halves ? kBM : 2 * kBM), n_q) - 1) - q_frame + 1;
+    const bool cols = !CACHE && !p.halves && nF <= 8 * D && q_frames <= BiasCols::FRAMES;
+
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(C::B_Q), 64);
         for (int s = 0; s < C::KST; ++s) {
-            ptx::mbar_init(bar(C::B_KFULL + s), C::FULL_COUNT);
+            ptx::mbar_init(bar(C::B_KFULL + s), C::FULL_COUNT + (cols ? 2 : 0));
             ptx::mbar_init(bar(C::B_KEMPTY + s), 1);
         }
         for (int s = 0; s < C::VST; ++s) {
@@ -358,8 +441,19 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     // the bias by distance, and the first and last distance that is visible
     int dlo, dhi;
     fill_bias(tab, p.bias, p.g.heads, head, C::THREADS, dlo, dhi);
+    if (!CACHE && cols) {
+        if (threadIdx.x < 2 * kBM) {
+            const int t = threadIdx.x / kBM, r = threadIdx.x % kBM;
+            BiasCols::store_query(sbase + C::OFF_QB + t * BiasCols::TILE_BYTES, r,
+                                  dF.div(min(q_first + (halves ? 0 : t * kBM) + r, n_q - 1)) - q_frame);
+            fence_proxy_async();
+        }
+    }
     ptx::tc_fence_before();
     __syncthreads();
+    if (!CACHE && cols)
+        for (int i = threadIdx.x; i < 2 * dmax + BiasCols::FRAMES; i += C::THREADS)
+            BiasCols::make_row(sbase + C::OFF_ROWS + i * BiasCols::ROW, tab, i - dmax - BiasCols::FRAMES + 1, dmax, p.scale_log2);
     dlo = __reduce_min_sync(0xffffffffu, dlo);
     dhi = __reduce_max_sync(0xffffffffu, dhi);
     if (lane == 0 && dlo <= dhi) {
@@ -460,6 +554,17 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     if (!(ok = wait_empty(is_v, j))) break;
                     const int s = j % (is_v ? C::VST : C::KST);
                     load_tile_rows<D>(sbase + (is_v ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES, is_v ? p.v : p.k, kv, pw, lane);
+                    if (cols && !is_v) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int r = 64 * pw + 32 * half + lane;
+                            BiasCols::store_key(sbase + C::OFF_KB + s * BiasCols::TILE_BYTES, r, sbase + C::OFF_ROWS,
+                                                q_frame - dF.div(min(jbeg + j * kBN + r, jend - 1)), dmax);
+                        }
+                        fence_proxy_async();  // these stores, for the tensor core
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(C::B_KFULL + s));
+                    }
                     // test hook: one thread never signals the first K tile
                     if (!(fault_skip && L == 0)) cp_async_arrive_noinc(bar((is_v ? C::B_VFULL : C::B_KFULL) + s));
                 }
@@ -478,12 +583,18 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 const uint64_t qd1 = ptx::smem_desc(q1, 16, 8 * C::SW, C::LAYOUT);
                 const uint64_t kd0 = ptx::smem_desc(sbase + C::OFF_K, 16, 8 * C::SW, C::LAYOUT);
                 const uint64_t vd0 = ptx::smem_desc(sbase + C::OFF_V, C::BOX_BYTES, 8 * C::SW, C::LAYOUT);
-                auto issue_s = [&](uint64_t qd, int kslot, uint32_t d_tmem) {
+                auto bias_desc = [&](int off) { return ptx::smem_desc(sbase + off, 16, 8 * BiasCols::ROW, BiasCols::LAYOUT); };
+                auto issue_s = [&](int qt, int kslot, uint32_t d_tmem) {
+                    const uint64_t qd = qt ? qd1 : qd0;
                     const uint64_t kd = kd0 + ((kslot * C::TILE_BYTES) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < C::KSTEPS; ++kk) {
                         const uint32_t off = C::kstep_off(kk) >> 4;
                         ptx::mma_ss(d_tmem, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    if (!CACHE && cols) {
+                        ptx::mma_ss(d_tmem, bias_desc(C::OFF_QB + qt * BiasCols::TILE_BYTES),
+                                    bias_desc(C::OFF_KB + kslot * BiasCols::TILE_BYTES), idesc_s, 1u);
                     }
                 };
                 auto issue_o = [&](int qt, int vslot, bool acc, int phase) -> bool {
@@ -508,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 if (ok) {
                     fence_proxy_async();  // cp.async data observed through the barriers, for the MMA
                     ptx::tc_fence_after();
-                    issue_s(qd0, 0, tmem + C::COL_S0);
+                    issue_s(0, 0, tmem + C::COL_S0);
                     ptx::mma_commit(bar(C::B_SFULL + 0));
                 }
                 if (halves) {
@@ -518,7 +629,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                         if (!ptx::mbar_wait(bar(C::B_KFULL + j % C::KST), (j / C::KST) & 1, abort, lim)) return false;
                         fence_proxy_async();
                         ptx::tc_fence_after();
-                        issue_s(qt ? qd1 : qd0, j % C::KST, tmem + (qt ? C::COL_S1 : C::COL_S0));
+                        issue_s(qt, j % C::KST, tmem + (qt ? C::COL_S1 : C::COL_S0));
                         ptx::mma_commit(bar(C::B_SFULL + qt));
                         ptx::mma_commit(bar(C::B_KEMPTY + j % C::KST));
                         return true;
@@ -535,7 +646,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     }
                 } else {
                     if (ok) {
-                        issue_s(qd1, 0, tmem + C::COL_S1);
+                        issue_s(1, 0, tmem + C::COL_S1);
                         ptx::mma_commit(bar(C::B_SFULL + 1));
                         ptx::mma_commit(bar(C::B_KEMPTY + 0));
                     }
@@ -556,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                             }
                             fence_proxy_async();
                             ptx::tc_fence_after();
-                            issue_s(qd0, ks, tmem + C::COL_S0);
+                            issue_s(0, ks, tmem + C::COL_S0);
                             ptx::mma_commit(bar(C::B_SFULL + 0));
                         }
                         if (!issue_o(1, vs, j > 0, j & 1)) {
@@ -565,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                         }
                         ptx::mma_commit(bar(C::B_VEMPTY + vs));
                         if (more) {
-                            issue_s(qd1, ks, tmem + C::COL_S1);
+                            issue_s(1, ks, tmem + C::COL_S1);
                             ptx::mma_commit(bar(C::B_SFULL + 1));
                             ptx::mma_commit(bar(C::B_KEMPTY + ks));
                         }
@@ -623,13 +734,13 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             const int j0 = jbeg + (halves ? 2 * j + qt : j) * kBN;
             const int f0 = dF.div(j0);
             const int border = (f0 + 1) * nF - j0;  // tile column where the next frame starts
-            float off = bias_of(f0), mul = sl2;     // scores are S * mul + off, in log2
+            float off = !CACHE && cols ? 0.f : bias_of(f0), mul = sl2;  // scores are S * mul + off, in log2
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(sfull, j & 1, abort, lim))) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            if (border < kBN) {
+            if (border < kBN && !(!CACHE && cols)) {
                 // A frame starts inside the tile: S becomes S * scale + bias in place, some columns at a
                 // time, before the softmax below reads the row. (Biases per 32 columns carried through
                 // the softmax instead cost the tiles without a border 18 %.)
@@ -724,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             // P = 2^(S*scale*log2(e) + bias - m), written as bf16 pairs over the first 64 columns of
             // S, in two halves released as they are stored. A row that has seen no key yet keeps
             // the reference 0, so that its -inf scores give 0.
-            const float neg = off - (m_run == -INFINITY ? 0.f : m_run) + (CACHE ? kPShift : 0.f);
+            const float neg = off - (m_run < -BiasCols::FAR_LOG2 ? 0.f : m_run) + (CACHE ? kPShift : 0.f);
             float2 sum_a = make_float2(0.f, 0.f), sum_b = sum_a;  // four short addition chains
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -776,6 +887,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         if (ok && (nkv == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_OFULL), 0, abort, lim)))) {
             ptx::tc_fence_after();
             // a row without a visible key: 0, and -inf for its log-sum-exp
+            if (!CACHE && m_run > BiasCols::FAR_LOG2) l_run = NAN;  // a bias that is not finite
             const float v_scale = CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f;
             float inv_l = l_run == 0.f ? 0.f : v_scale / l_run;
             float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run) - (CACHE ? kPShift : 0.f);

@@ -121,6 +121,61 @@ def test_table_entries_that_mask(fps):
     assert grads[3][1, 0] == 0 and grads[3][3, 1] == 0
 
 
+# calls of enough query tiles for 256-query CTAs, where the tensor core adds the bias of frames of 64 .. 8d tokens
+WIDE = [
+    ((1, 4, 9, 10, 64, 32), 1, 0, 2, (8, 3, True, None)),       # 90 tokens a frame, five frames a CTA
+    ((2, 6, 10, 13, 32, 64), 2, 1, 1, (9, 255, False, 4)),      # Skiparse-1D, frames of up to 36: ten a CTA
+    ((1, 3, 13, 17, 60, 64), 1, 0, 2, (5, 1, False, None)),     # 221 tokens, a last CTA of 151
+    ((1, 2, 19, 22, 70, 128), 1, 1, 2, (3, 4, True, None)),     # 418 tokens
+    ((3, 5, 16, 18, 16, 128), 2, 0, 2, (7, 6, False, 3)),       # 72 tokens, window
+    ((1, 5, 8, 16, 60, 32), 1, 0, 2, (1, 0, False, None)),      # D = 0: one bias for all
+]
+
+
+@pytest.mark.parametrize("scale", [1.0, 12.0])  # entries up to 40: their sum with q.k in fp32 keeps within 2^-13
+@pytest.mark.parametrize("shape,P,mode,dims,bias", WIDE, ids=["x".join(map(str, s[0])) for s in WIDE])
+def test_forward_of_many_queries(fps, shape, P, mode, dims, bias, scale):
+    q, k, v, _, table, buckets = inputs(shape, *bias)
+    table = (table * scale).contiguous()
+    out, lse = api(fps, "attn_relbias_fwd", dims)(q, k, v, table, buckets, P, mode)
+    assert fps.get_device_status() == 0
+    want = reference(q, k, v, table, buckets, P, mode, dims)
+    check("out", out, *want["out"])
+    check("lse", lse, *want["lse"])
+
+
+@pytest.mark.parametrize("shape", [(1, 4, 9, 10, 64, 32), (1, 4, 6, 10, 2, 64)])
+@pytest.mark.parametrize("wild", [float("inf"), float("nan")])
+def test_entries_that_are_not_finite(fps, shape, wild):
+    """A bucket of +inf or NaN makes the rows that see it NaN, and no others."""
+    q, k, v, _, table, _ = inputs(shape, 4, 3)
+    causal = torch.tensor([-1, -1, -1, 0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    table[2, ::2] = wild
+    out, _ = fps.skiparse2d_attn_relbias_fwd(q, k, v, table, causal, 1, 0)
+    assert fps.get_device_status() == 0
+    assert torch.isnan(out[:, 2:, :, :, ::2].float()).all()
+    table[2, ::2] = 0
+    want, tol = reference(q, k, v, table, causal, 1, 0)["out"]
+    check("out", out[:, :2], want[:, :2], tol[:, :2])
+    check("out", out[:, :, :, :, 1::2], want[:, :, :, :, 1::2], tol[:, :, :, :, 1::2])
+
+
+def test_wide_masks_that_leave_rows_empty(fps):
+    """As below, in a call of many queries: only later frames visible, or nothing."""
+    shape = (1, 4, 9, 10, 64, 32)
+    q, k, v, _, table, _ = inputs(shape, 4, 3)
+    later = torch.tensor([0, 1, 2, -1, -1, -1, -1], dtype=torch.int32, device="cuda")
+    out, lse = fps.skiparse2d_attn_relbias_fwd(q, k, v, table, later, 1, 0)
+    want = reference(q, k, v, table, later, 1, 0)
+    check("out", out, *want["out"])
+    check("lse", lse, *want["lse"])
+    assert (out[:, 3] == 0).all() and (lse[:, 3] == -float("inf")).all()
+    low = torch.full_like(table, torch.finfo(torch.bfloat16).min)
+    out, lse = fps.skiparse2d_attn_relbias_fwd(q, k, v, low, later, 1, 0)
+    assert fps.get_device_status() == 0
+    assert (out == 0).all() and (lse == -float("inf")).all()
+
+
 def test_no_mask_and_zero_table_is_the_plain_forward(fps):
     """A zero table without masks says what the plain forward says."""
     for shape, P in (((1, 2, 16, 16, 2, 128), 1), ((2, 3, 10, 14, 2, 64), 2)):
