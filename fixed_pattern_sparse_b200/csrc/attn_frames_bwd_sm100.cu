@@ -26,7 +26,12 @@
 //     eight tables, in a fixed order, to the workspace, and the last kernel adds those rows and
 //     joins distances to buckets, in a fixed order too: the result does not depend on timing.
 //     Per score this costs one addition (half of one packed instruction).
-// Launches: row statistics (D, L in log2, the bias by head and distance), dQ, dK/dV, dtable.
+// Launches: dQ, which first takes D and L from its rows of out, dO and lse; dK/dV; dtable. (Row statistics
+// by a kernel of their own took the same at 480p and 7 us longer, of 183 and of 94, in small steps.)
+// What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): dQ 2.2 ms, dK and dV 3.3 ms,
+// 0.98 and 0.87 PFLOP/s. As in the unbiased backward pass, a key step waits on its chain of products and
+// exponentials (2500 and 3600 clocks at d = 64, where the tensor core needs 770 and 1020 of them); the
+// frames add 7 % more streamed rows to dK and dV, and the sums of dS.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -59,7 +64,8 @@ struct BwdCfg : TileGeom<D> {
     static constexpr int OFF_VEC = OFF_B2 + NS2 * TILE_BYTES;  // [B1 slot or stationary][L,D][128] fp32
     static constexpr int VEC_BYTES = (KV ? NS1 : 1) * 2 * kTileRows * 4;
     static constexpr int OFF_HIST = OFF_VEC + VEC_BYTES;       // key-major: 8 warps x distances
-    static constexpr int OFF_BAR = OFF_HIST + (KV ? 8 * (kMaxDistEntries + 1) * 4 : 0);
+    static constexpr int OFF_TAB = OFF_HIST + (KV ? 8 * (kMaxDistEntries + 1) * 4 : 0);  // the bias by distance, bf16
+    static constexpr int OFF_BAR = OFF_TAB + 2 * (kMaxDistEntries + 1);
     static constexpr int B_STAT = 0, B_FULL1 = 1, B_EMPTY1 = B_FULL1 + NS1, B_FULL2 = B_EMPTY1 + NS1,
                          B_EMPTY2 = B_FULL2 + NS2, B_X1 = B_EMPTY2 + NS2, B_X2 = B_X1 + 1, B_X1FREE = B_X2 + 1,
                          B_P = B_X1FREE + 1, B_DS = B_P + 1, B_ACC = B_DS + 1,
@@ -68,10 +74,11 @@ struct BwdCfg : TileGeom<D> {
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
     static constexpr int OFF_RANGE = OFF_ABORT + 4;            // first and last visible distance
     static constexpr int SMEM_USED = OFF_RANGE + 8;
-    // + slack for 1024-byte alignment; at least 116 KB so that one CTA (and its 512 TMEM
-    // columns) owns an SM even for small d
-    static constexpr int SMEM_BYTES = SMEM_USED + 1024 > 118784 ? SMEM_USED + 1024 : 118784;
-    static_assert(SMEM_BYTES <= kMaxSmem, "shared memory overflow");
+    // + slack for 1024-byte alignment where it fits (the kernel checks the slack it got); at least
+    // 116 KB so that one CTA (and its 512 TMEM columns) owns an SM even for small d
+    static constexpr int SMEM_BYTES =
+        SMEM_USED + 1024 > kMaxSmem ? kMaxSmem : (SMEM_USED + 1024 > 118784 ? SMEM_USED + 1024 : 118784);
+    static_assert(SMEM_USED + 256 <= kMaxSmem, "shared memory overflow");
     // TMEM: X1 = S (or S^T), X2 = dP (or dP^T); P^T (key-major) and dS (both kernels) are written
     // in bf16 over the first half of each warpgroup's 64 columns of X1 and X2
     static constexpr uint32_t COL_X1 = 0, COL_X2 = 128, COL_ACC1 = 256, COL_ACC2 = 256 + D, NCOLS = 512;
@@ -101,6 +108,26 @@ __device__ __forceinline__ float2 ds_pair(float2 p, float2 d, uint32_t dp0, uint
     return __fmul2_rn(p, __ffma2_rn(d, make_float2(-1.f, -1.f), make_float2(__uint_as_float(dp0), __uint_as_float(dp1))));
 }
 
+// sum_e dO[e] * (O[e] + O_lo[e]) over a row that `lanes` neighbouring lanes hold, eight elements each, this
+// lane's from element `at` of the tensors.
+__device__ __forceinline__ float dot_of_row(const uint16_t* out, const uint16_t* out_lo, const uint16_t* dout, long long at,
+                                            int lanes) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(out + at));
+    const uint4 g = __ldg(reinterpret_cast<const uint4*>(dout + at));
+    uint4 lo = make_uint4(0u, 0u, 0u, 0u);
+    if (out_lo) lo = __ldg(reinterpret_cast<const uint4*>(out_lo + at));
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w}, lv[4] = {lo.x, lo.y, lo.z, lo.w};
+    float acc = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        acc = fmaf(__uint_as_float(av[e] << 16) + __uint_as_float(lv[e] << 16), __uint_as_float(gv[e] << 16), acc);
+        acc = fmaf(__uint_as_float(av[e] & 0xffff0000u) + __uint_as_float(lv[e] & 0xffff0000u),
+                   __uint_as_float(gv[e] & 0xffff0000u), acc);
+    }
+    for (int off = lanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    return acc;
+}
+
 template <int D, bool KV, bool AL>
 __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(const FramesBwdParams p) {
     using C = BwdCfg<D, KV>;
@@ -120,6 +147,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+    if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {
+        // not aligned well enough for this layout (uniform over the CTA, before any shared state): report
+        // it instead of running out of bounds
+        if (threadIdx.x == 0) atomicExch(p.status, kErrLaunch);
+        return;
+    }
     uint8_t* smem = smem_raw + pad;
     const uint32_t sbase = raw_base + pad;
     auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
@@ -133,7 +166,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
     const int lane = threadIdx.x & 31;
     const uint64_t lim = p.wait_limit_ns;
     const int dmax = p.bias.D;
-    const float* bias2 = p.bias2 + static_cast<size_t>(head) * (2 * dmax + 1) + dmax;  // by distance
+    uint16_t* tab = reinterpret_cast<uint16_t*>(smem + C::OFF_TAB) + dmax;  // bias by distance, bf16 as in the table
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(C::B_STAT), kBwdProducers);
@@ -171,19 +204,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         const int pair = (warp - kBwdProd0) >> 1, pw = (warp - kBwdProd0) & 1;
         const TileRows ta = tile_rows(rows, first, n_c, pw, lane, p.nrows, p.status);
         load_tile_rows<D>(sbase + (pair ? C::OFF_A2 : C::OFF_A1), pair ? g_a2 : g_a1, ta, pw, lane);
-        if (!KV && pair == 0) {  // the stationary queries' L and D
-            load_vec(sbase + C::OFF_VEC, p.nlse2, ta, pw, lane);
-            load_vec(sbase + C::OFF_VEC + 4 * kTileRows, p.delta, ta, pw, lane);
-        }
     }
     if (KV)
         for (int i = threadIdx.x; i < 8 * p.ND; i += kBwdThreads) hist[i] = 0.f;
     int dlo = dmax + 1, dhi = -dmax - 1;  // first and last visible distance
-    for (int u = static_cast<int>(threadIdx.x) - dmax; u <= dmax; u += kBwdThreads)
-        if (__ldg(bias2 + u) != -INFINITY) {
+    for (int u = static_cast<int>(threadIdx.x) - dmax; u <= dmax; u += kBwdThreads) {
+        const uint16_t b = bias_bf16(p.bias, p.g.heads, u + dmax, head);
+        tab[u] = b;
+        if (b != kBiasNone) {
             dlo = min(dlo, u);
             dhi = max(dhi, u);
         }
+    }
     dlo = __reduce_min_sync(0xffffffffu, dlo);
     dhi = __reduce_max_sync(0xffffffffu, dhi);
     ptx::tc_fence_before();
@@ -367,7 +399,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         const int t_row = dF.div(min(first + row, n_c - 1));
         const bool one_frame = __all_sync(0xffffffffu, t_row == __shfl_sync(0xffffffffu, t_row, 0));  // of this warp's rows
         // bias of this row and streamed frame f
-        auto bias_of = [&](int f) { return __ldg(bias2 + clamp_dist(KV ? f - t_row : t_row - f, dmax)); };
+        auto bias_of = [&](int f) {
+            return __uint_as_float(static_cast<uint32_t>(tab[clamp_dist(KV ? f - t_row : t_row - f, dmax)]) << 16) * kLog2E;
+        };
         // Key-major: adds v, this row's sum of dS over queries of frame f, to the warp's table of
         // distances. Rows of equal distance are neighbours: their sum forms in the first of them.
         float* my_hist = hist + warp * p.ND;
@@ -392,7 +426,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
         };
         float acc = 0.f;   // sum of dS over the queries of frame f_acc so far
         int f_acc = -1;
-        float row_l2 = 0.f, row_d = 0.f;
+        float row_l2 = 0.f, row_d = 0.f;  // query-major: -L in log2, and D
+        if (!KV) {
+            // D of the tile's rows, from memory while the first keys travel: D / 8 lanes a row, 16 rows a warp
+            float* d_of = reinterpret_cast<float*>(smem + C::OFF_VEC);
+            constexpr int LPR = D / 8, RPW = 32 / LPR;
+#pragma unroll 4
+            for (int i = 0; i < 16; i += RPW) {
+                const int r = warp * 16 + i + lane / LPR;
+                const long long at = load_row(rows(min(first + r, n_c - 1)), p.nrows, p.status) * D + (lane % LPR) * 8;
+                const float d = dot_of_row(p.out, p.out_lo, p.dout, at, LPR);
+                if (lane % LPR == 0) d_of[r] = d;
+            }
+            const long long at = load_row(rows(min(first + row, n_c - 1)), p.nrows, p.status);
+            const float l = __ldg(p.lse + at) * kLog2E;
+            row_l2 = l < kLse2Low ? -kLse2Low : -l;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            row_d = d_of[row];
+            if (h == 0 && row_real) p.nlse2[at] = row_l2;
+        }
         float2 row_sum = make_float2(0.f, 0.f);  // query-major: of the row's dS
         bool ok = true;
         // the frame of the next column, the columns until the frame after it starts, and the bias
@@ -411,14 +463,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
             }
             ptx::tc_fence_after();
             // the L/D vectors were written by the producers' cp.async: observe their barrier too
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(KV ? bar(C::B_FULL1 + s1) : bar(C::B_STAT),
-                                                        KV ? (j / C::NS1) & 1 : 0, abort, lim))) {
+            if (KV && !__all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_FULL1 + s1), (j / C::NS1) & 1, abort, lim))) {
                 ok = false;
                 break;
-            }
-            if (!KV && j == 0) {
-                row_l2 = vecs[row];
-                row_d = vecs[kTileRows + row];
             }
             const float* col_l = vecs + s1 * 2 * kTileRows + 64 * h;   // key-major: per column
             const float* col_d = col_l + kTileRows;
@@ -605,10 +652,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
             const int si = first + row;                 // stationary row (key or query)
             const bool store = si < n_c && row_ok(rows(si), p.nrows, p.status);
             const size_t grow = store ? static_cast<size_t>(rows(si)) : 0;
-            if (!KV && nstream > 0) {
+            if (!KV) {
                 // The row's dS ought to sum to zero; what it sums to is D's error, which goes into D
                 // for the key-major kernel.
-                float* other = reinterpret_cast<float*>(smem + C::OFF_VEC) + row;  // over the rows' L, long read
+                float* other = reinterpret_cast<float*>(smem + C::OFF_VEC) + kTileRows + row;
                 if (h == 1) *other = row_sum.x + row_sum.y;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (h == 0 && store) p.delta[grow] = row_d + ((row_sum.x + row_sum.y) + *other);
@@ -641,8 +688,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
                     }
                 }
             }
-        } else if (!*abort) {
-            record_abort(abort, p.status);
+        } else {
+            if (!*abort) record_abort(abort, p.status);
+            if (!KV) asm volatile("bar.arrive 1, 256;" ::: "memory");  // for warps that saw no failure
         }
     }
 
@@ -662,44 +710,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
             part[u * n] = s;
         }
     }
-}
-
-// D[row] = sum_e dO[row][e] * (O[row][e] + O_lo[row][e]) (16 lanes per 256-byte row, fewer for smaller d), the row's
-// negated log-sum-exp in log2, and the bias by head and distance in log2.
-template <int D>
-__global__ void __launch_bounds__(256) skiparse_frames_stats_kernel(const FramesBwdParams p, long long nrows) {
-    constexpr int LPR = D / 8;            // lanes per row (8 bf16 = 16 bytes per lane)
-    constexpr int RPW = 32 / LPR;         // rows per warp step
-    const int lane = threadIdx.x & 31;
-    const long long thread = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long r0 = (thread >> 5) * RPW; r0 < nrows; r0 += (nthreads >> 5) * RPW) {
-        const long long r = r0 + lane / LPR;
-        float acc = 0.f;
-        if (r < nrows) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p.out + r * D + (lane % LPR) * 8);
-            const uint4 g = *reinterpret_cast<const uint4*>(p.dout + r * D + (lane % LPR) * 8);
-            uint4 lo = make_uint4(0u, 0u, 0u, 0u);
-            if (p.out_lo) lo = *reinterpret_cast<const uint4*>(p.out_lo + r * D + (lane % LPR) * 8);
-            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w}, lv[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc = fmaf(__uint_as_float(av[e] << 16) + __uint_as_float(lv[e] << 16), __uint_as_float(gv[e] << 16), acc);
-                acc = fmaf(__uint_as_float(av[e] & 0xffff0000u) + __uint_as_float(lv[e] & 0xffff0000u),
-                           __uint_as_float(gv[e] & 0xffff0000u), acc);
-            }
-        }
-#pragma unroll
-        for (int off = LPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-        if (r < nrows && lane % LPR == 0) {
-            p.delta[r] = acc;
-            const float l = p.lse[r] * kLog2E;
-            p.nlse2[r] = l < kLse2Low ? -kLse2Low : -l;
-        }
-    }
-    const int entries = 2 * p.bias.D + 1;
-    for (long long i = thread; i < static_cast<long long>(p.g.heads) * entries; i += nthreads)
-        p.bias2[i] = bias_log2(p.bias, p.g.heads, static_cast<int>(i % entries), static_cast<int>(i / entries));
 }
 
 // dtable of one head: the CTAs' sums added per distance (one warp each), then the distances of each
@@ -765,17 +775,7 @@ bool aligned_chunks(int nF) { return (nF + 31) / 32 * 32 <= nF * 2; }
 
 template <int D>
 int launch_bwd_all(const FramesBwdParams& p, const Geometry& g, cudaStream_t st) {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long long nrows = static_cast<long long>(g.B) * g.T * g.H * g.W * g.heads;
-    const long long rows_per_block = 8LL * (32 / (D / 8));
-    long long blocks = (nrows + rows_per_block - 1) / rows_per_block;
-    if (blocks > 16LL * sms) blocks = 16LL * sms;
-    skiparse_frames_stats_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p, nrows);
-    int e = static_cast<int>(cudaGetLastError());
-    if (e) return e;
-    e = launch_bwd_d<D, false, false>(p, g, st);
+    int e = launch_bwd_d<D, false, false>(p, g, st);
     if (e) return e;
     e = aligned_chunks(max_class_tokens(g)) ? launch_bwd_d<D, true, true>(p, g, st) : launch_bwd_d<D, true, false>(p, g, st);
     if (e) return e;

@@ -10,8 +10,9 @@
 // S = Q K^T and O += P V run on tcgen05 with S, P and O in TMEM, one thread per query row does
 // the online softmax with the lazy rescale. What the frames add:
 //   * The bias is constant over the tokens of a frame, so a key tile inside one frame needs one table
-//     lookup per row, folded into the softmax's existing FMA: no instruction per score. A tile
-//     that holds a frame's border gets its biases by a pass over S in TMEM before the softmax.
+//     lookup per row, folded into the softmax's existing FMA: no instruction per score. For tiles
+//     that hold a frame's border the bias comes as further columns of Q and K (bf16 keys, frames of
+//     64 tokens and more: BiasCols below), or by a pass over S in TMEM before the softmax.
 //   * The frames that some row of the CTA can see form a range, from the first and last visible
 //     distance of the table; only its keys are loaded. With a causal map that is half the work.
 //     Query tiles are launched last frame first, so that the longest ones start first.
@@ -30,7 +31,12 @@
 //   * Calls of few query tiles: a CTA may own 128 queries instead, its two softmax groups taking
 //     every other key tile each (an own O in TMEM each, joined at the end), which halves the
 //     length of a CTA and doubles their number.
-// Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB, staging 32 KB.
+// Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB, staging (cache) 32 KB or bias
+// columns (bf16) 32 KB.
+// What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): 1.44 ms for 1.65 TFLOP, 1140
+// TFLOP/s. A key step of 256 queries takes 3100 to 3500 clocks against 2048 of tensor core and as many of
+// exponentials; the rest is the dependency of the two tiles' softmax and products on each other. The
+// cache form adds the expansion of the codes: 0.65 ms for three frames over 24 (790 TFLOP/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -973,8 +979,9 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                     }
                 }
             }
-        } else if (!*abort) {
-            record_abort(abort, p.status);
+        } else {
+            if (!*abort) record_abort(abort, p.status);
+            if (halves && nkv > 1) asm volatile("bar.arrive 1, 256;" ::: "memory");  // for warps that saw no failure
         }
     }
 

@@ -88,10 +88,9 @@ int relbias_fwd(int dims, const void* q, const void* k, const void* v, const voi
 }
 
 // Workspace of the backward pass, in order (each part 256-byte aligned): D and lse * log2(e) of
-// every row, the bias by head and distance, the sums of dS by head, distance, subsequence and
-// key tile.
+// every row, the sums of dS by head, distance, subsequence and key tile.
 struct BwdSpace {
-    size_t lse2, bias2, part, bytes;
+    size_t lse2, part, bytes;
     int Dn, ND, tiles;
 };
 
@@ -105,8 +104,7 @@ BwdSpace bwd_space(const Geometry& g, int max_distance) {
     w.tiles = static_cast<int>((n + 127) / 128);
     const size_t rows = static_cast<size_t>(g.B) * g.T * g.H * g.W * g.heads;
     w.lse2 = pad256(rows * 4);
-    w.bias2 = w.lse2 + pad256(rows * 4);
-    w.part = w.bias2 + pad256(static_cast<size_t>(g.heads) * (2 * max_distance + 1) * 4);
+    w.part = w.lse2 + pad256(rows * 4);
     w.bytes = w.part + pad256(static_cast<size_t>(g.heads) * g.B * g.Ph * g.Pw * w.tiles * w.ND * 4);
     return w;
 }
@@ -155,7 +153,6 @@ int relbias_bwd(int dims, const void* q, const void* k, const void* v, const voi
     p.lse = lse;
     p.delta = reinterpret_cast<float*>(ws);
     p.nlse2 = reinterpret_cast<float*>(ws + w.lse2);
-    p.bias2 = reinterpret_cast<float*>(ws + w.bias2);
     p.part = reinterpret_cast<float*>(ws + w.part);
     p.dtable = static_cast<uint16_t*>(dtable);
     p.dq = static_cast<uint16_t*>(dq);

@@ -12,13 +12,17 @@ namespace skiparse {
 
 constexpr float kLog2E = 1.4426950408889634f;
 
-// Bias of distance index u (0..2D) for one head in units of log2, -inf where masked.
-__device__ __forceinline__ float bias_log2(const FrameBias& fb, int heads, int u, int head) {
-    if (!fb.table) return 0.f;
+// Bias of distance index u (0..2D) for one head as the table's bf16, kBiasNone (-inf) where masked.
+constexpr uint16_t kBiasNone = 0xff80;
+__device__ __forceinline__ uint16_t bias_bf16(const FrameBias& fb, int heads, int u, int head) {
     const int g = fb.buckets[u];
-    if (g < 0 || g >= fb.NB) return -INFINITY;
-    const float b = __uint_as_float(static_cast<uint32_t>(fb.table[static_cast<size_t>(g) * heads + head]) << 16);
-    return b < kBiasMasked ? -INFINITY : b * kLog2E;
+    if (g < 0 || g >= fb.NB) return kBiasNone;
+    const uint16_t b = fb.table[static_cast<size_t>(g) * heads + head];
+    return __uint_as_float(static_cast<uint32_t>(b) << 16) < kBiasMasked ? kBiasNone : b;
+}
+// The same in units of log2, -inf where masked; 0 without a table.
+__device__ __forceinline__ float bias_log2(const FrameBias& fb, int heads, int u, int head) {
+    return fb.table ? __uint_as_float(static_cast<uint32_t>(bias_bf16(fb, heads, u, head)) << 16) * kLog2E : 0.f;
 }
 
 __device__ __forceinline__ int clamp_dist(int u, int D) { return min(max(u, -D), D); }

@@ -90,9 +90,8 @@ struct FramesBwdParams {
     const uint16_t* out_lo;  // optional
     const uint16_t* dout;
     const float* lse;
-    float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo)), then corrected by the dQ kernel
-    float* nlse2;      // workspace (rows): -lse * log2(e), at most -kLse2Low
-    float* bias2;      // workspace (heads, 2D+1): bias * log2(e), -inf where masked
+    float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo)), corrected, by the dQ kernel
+    float* nlse2;      // workspace (rows): -lse * log2(e), at most -kLse2Low, by the dQ kernel
     float* part;       // workspace (heads, ND, seqs, tiles): sums of dS by frame distance
     uint16_t* dtable;  // bf16 (NB, heads)
     uint16_t* dq;

@@ -312,7 +312,7 @@ SKIPARSE_API int skiparse1d_attn_relbias_fwd(const void* q, const void* k, const
  *            and nothing in it is used after the call. Calls that can run at the same time (on
  *            other streams, or as replays of graphs captured separately) need workspaces of
  *            their own.
- * Four kernel launches (row statistics, dq, dk/dv, dtable), no atomics on results: deterministic.
+ * Three kernel launches (dq, dk/dv, dtable), no atomics on results: deterministic.
  */
 SKIPARSE_API int skiparse2d_attn_relbias_bwd(const void* q, const void* k, const void* v, const void* out,
                                              const void* out_lo, const void* dout, const float* lse,
