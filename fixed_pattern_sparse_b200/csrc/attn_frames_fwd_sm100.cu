@@ -746,8 +746,13 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 break;
             }
             ptx::tc_fence_after();
-            if (border < kBN && !(!CACHE && cols)) {
-                // A frame starts inside the tile: S becomes S * scale + bias in place, some columns at a
+            // Whether a frame starts inside the tile, and with another bias (for some row of this warp; distances
+            // that share a bucket are common): d = 64 and 32, 40 and 64 frames, 910 -> 859 and 682 -> 620 us. At
+            // d = 128 the second question costs more than it saves (480p chunk 636 -> 698 us).
+            bool mixed = border < kBN && (CACHE ? p.bias.table != nullptr : !cols);
+            if (CACHE && D < 128 && mixed && border + nF >= kBN) mixed = __any_sync(0xffffffffu, bias_of(f0 + 1) != off);
+            if (mixed) {
+                // S becomes S * scale + bias in place, some columns at a
                 // time, before the softmax below reads the row. (Biases per 32 columns carried through
                 // the softmax instead cost the tiles without a border 18 %.)
                 if (nF >= 32) {  // at most one border in 32 columns
