@@ -289,7 +289,7 @@ int attn_cached(int dims, const void* q, const void* k_cache, const void* v_cach
     p.cache = cache_view(g, k_cache, v_cache, k_scale, v_scale, start, capacity);
     p.scale_log2 = static_cast<float>(log2e_over_sqrt(d));
     p.wait_limit_ns = api::wait_limit_ns();
-    p.fault = api::pending_fault(1);
+    p.fault = skiparse::cached_small(g) ? 0 : api::pending_fault(1);  // the few-query kernel has no waits
     p.nrows = api::debug_bound(rows);
     const int e = skiparse::launch_frames_fwd(p, g, stream);
     return e == 0 ? SKIPARSE_OK : api::cuda_fail(e);

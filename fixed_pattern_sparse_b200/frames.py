@@ -206,7 +206,8 @@ def skiparse2d_attn_relbias_fwd(q, k, v, table, buckets, P: int, mode: int, out=
 
     q, k, v, out: (B,T,H,W,heads,d) bf16; table: (num_buckets, heads) bf16; buckets:
     (2*max_distance+1) int32, the bucket of each frame distance t_q - t_k (frame_buckets makes the
-    usual map), a value outside [0, num_buckets) masking it; lse: (B,T,H,W,heads) fp32, natural
+    usual map), a value outside [0, num_buckets) masking it (keys and values have to be finite there
+    too); lse: (B,T,H,W,heads) fp32, natural
     log; out_lo: an optional bf16 tensor like q that receives what rounding took from out, for a more
     exact backward pass. A row without a visible key gives 0 and lse -inf."""
     return _relbias_fwd(2, q, k, v, table, buckets, P, mode, out, lse, out_lo, stream)
@@ -247,6 +248,7 @@ class SkiparseRelBiasAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, table, buckets, out, lse, out_lo = ctx.saved_tensors
         grads = _relbias_bwd(ctx.dims, q, k, v, out, dout.contiguous(), lse, table, buckets, ctx.P, ctx.mode,
@@ -341,8 +343,10 @@ def skiparse2d_attn_cached(q, cache: FrameCache, start, P: int, mode: int, table
                            workspace=None, stream=None) -> torch.Tensor:
     """Attention of the newest T frames' queries over the cache, to which these frames have been
     appended with the same `start`; table and buckets as in skiparse2d_attn_relbias_fwd, or none.
-    A sequence with a negative start leaves its rows of `out` as they were. `lse`: an optional
-    (B,T,H,W,heads) fp32 tensor that receives the log-sum-exp."""
+    A sequence with a negative start leaves its rows of `out` as they were (so pass one: those of a
+    new tensor are not set). `lse`: an optional (B,T,H,W,heads) fp32 tensor that receives the
+    log-sum-exp. `workspace`: an optional CUDA uint8 tensor of
+    skiparse2d_attn_cached_workspace_bytes() bytes."""
     return _attn_cached(2, q, cache, start, P, mode, table, buckets, out, lse, workspace, stream)
 
 

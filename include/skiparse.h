@@ -277,7 +277,8 @@ SKIPARSE_API long long skiparse1d_rearranged_numel(int B, int T, int H, int W, i
  *   buckets : (2D+1) int32 on the device, 4-byte aligned. A value outside [0, num_buckets) masks
  *             the pair: -1 for u < 0 is the frame-causal mask, -1 for |u| >= w a window.
  *   table   : (num_buckets, heads) bf16, 2-byte aligned. An entry below -1e30 (-inf and the type's
- *             lowest value among them) masks like a bucket outside the range.
+ *             lowest value among them) masks like a bucket outside the range. Other entries keep within
+ *             +-1e30; one that is +inf or NaN makes the rows that see it NaN.
  * A query row without a visible key gives 0, lse -inf, and zero gradients. Masks act on scores:
  * keys and values at masked places have to be finite, as everywhere else.
  */

@@ -239,6 +239,15 @@ def test_autograd(fps):
             check(name, x.grad, *want[name])
 
 
+def test_second_derivatives_are_refused(fps):
+    q, k, v, _, table, buckets = inputs((1, 2, 4, 4, 1, 32), 2, 1)
+    leaf = q.requires_grad_()
+    (grad,) = torch.autograd.grad(fps.skiparse_attention(leaf, k, v, 1, 0, table=table, buckets=buckets).float().square().sum(), leaf,
+                                  create_graph=True)
+    with pytest.raises(RuntimeError):
+        grad.float().sum().backward()
+
+
 def test_captured_forward_and_backward(fps):
     """The entry points captured into a graph, while an eager graph of the same leaves lives; the
     replay on new inputs gives what the eager calls give."""
