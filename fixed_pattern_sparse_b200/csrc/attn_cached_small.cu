@@ -2,7 +2,7 @@
 //
 // Frame by frame, a class of a small latent has one or a few dozen queries, and what bounds the
 // call is reading the cache: two codes per key and value of d. The tcgen05 kernel would expand
-// every key into shared memory for tiles that are mostly empty. Here a warp keeps 16 query rows in
+// every key into shared memory for tiles that are mostly empty. Here a warp keeps 8 to 32 queries in
 // registers and walks over groups of 16 keys with m16n8k16 products (legacy tensor-core path;
 // the codes never leave registers after their copy), keys as the products' 16 rows and queries as
 // their 8 columns, so that a call of up to 8 queries a class wastes no product:
@@ -20,7 +20,9 @@
 //     reads: no barrier in the loop, 8 KB in flight per warp at d = 128.
 // What bounds it: reading the cache, as long as a step's instructions (conversions foremost: 64 per
 // lane and step at d = 128, 4 clocks each) keep below the 180 clocks in which an SM's share
-// of HBM delivers its 4 KB.
+// of HBM delivers its 4 KB. Measured, d = 128, one query a class, 192 classes and heads of 8000 keys (396 MB):
+// 88 us, 4.5 TB/s; d = 64, 12 to 20 queries a class, 64 of 4000 to 6700 keys (43 MB): 29 us, the latency of
+// 12 warps an SM.
 // Key groups are dealt to the warps of a CTA and, over long caches, to `splits` CTAs; warps join
 // through shared memory, CTAs through the join kernel of attn_frames_fwd_sm100.cu. A CTA has
 // 8, 16, 24 or 32 queries.

@@ -3,15 +3,17 @@
 // For every class, head and new frame, each block of 64 class tokens x d values shares a scale
 // 2^e, e the smallest whole number with max|x| <= 448 * 2^e (448: e4m3's largest value; e at
 // least -110), and is stored as codes RNE(x / 2^e): one rounding, of half a step of e4m3. A
-// power of two makes the scaling exact in both directions, and the attention kernel can give
-// code * 2^e to the tensor cores as bf16 without a second rounding. A block that holds an
+// power of two makes the scaling exact in both directions, and the attention kernels can give
+// the codes to the tensor cores as f16 without a second rounding. A block that holds an
 // infinity or a NaN is stored with a NaN scale.
 //
 // HBM-bound: 2 bytes read and 1 written per value. One CTA of 256 threads per block and head of
 // K or V holds the block's 64 * d values in registers (16-byte loads; a token's d values are one
 // contiguous row of its head) between the maximum and the conversion, so the input is read once.
 // Heads are the fastest grid dimension: CTAs that run together read the neighbouring heads of
-// the same tokens, and write 64 * d contiguous bytes each.
+// the same tokens, and write 64 * d contiguous bytes each. Eight CTAs an SM, which takes at most 32
+// registers a thread: at 36, one CTA fewer, both cases below took a third longer. Measured: a 720p frame
+// (111 MB moved) 18 us, 6.1 TB/s; two 480p clips of 21 frames (604 MB) 96 us, 6.3 TB/s.
 #include <cuda_runtime.h>
 
 #include "frames_common.cuh"

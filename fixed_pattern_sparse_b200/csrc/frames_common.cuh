@@ -1,5 +1,5 @@
 // frames_common.cuh -- device code shared by the frame-aware attention kernels: the bias by
-// frame distance, the frames that a tile of keys covers, and the reading of e4m3 codes as bf16.
+// frame distance, the frames that a tile of keys covers, and the reading of e4m3 codes as f16.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -161,7 +161,7 @@ def test_entries_that_are_not_finite(fps, shape, wild):
 
 
 def test_wide_masks_that_leave_rows_empty(fps):
-    """As below, in a call of many queries: only later frames visible, or nothing."""
+    """As above, in a call of many queries: only later frames visible, or nothing."""
     shape = (1, 4, 9, 10, 64, 32)
     q, k, v, _, table, _ = inputs(shape, 4, 3)
     later = torch.tensor([0, 1, 2, -1, -1, -1, -1], dtype=torch.int32, device="cuda")
