@@ -132,9 +132,9 @@ template <int D, bool KV, bool AL>
 __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(const FramesBwdParams p) {
     using C = BwdCfg<D, KV>;
     // the tiles that see most come first under a causal map: early keys, late queries
-    const int tile = KV ? blockIdx.x : gridDim.x - 1 - blockIdx.x;
-    const int head = blockIdx.y;
-    const int seq = blockIdx.z;
+    int tile, head, seq;
+    p.order.get(blockIdx.x, p.g.heads, tile, seq, head);
+    if (!KV) tile = p.tiles - 1 - tile;
     ClassView cls;
     cls.init(p.g, seq);
     const int nF = cls.nF;
@@ -762,7 +762,7 @@ int launch_bwd_d(const FramesBwdParams& p, const Geometry& g, cudaStream_t strea
         if (e != cudaSuccess) return static_cast<int>(e);
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
-    const dim3 grid(p.tiles, g.heads, p.seqs);
+    const dim3 grid(static_cast<unsigned>(p.tiles * g.heads * p.seqs));
     skiparse_frames_bwd_kernel<D, KV, AL><<<grid, kBwdThreads, C::SMEM_BYTES, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
 }

@@ -15,7 +15,7 @@
 //     64 tokens and more: BiasCols below), or by a pass over S in TMEM before the softmax.
 //   * The frames that some row of the CTA can see form a range, from the first and last visible
 //     distance of the table; only its keys are loaded. With a causal map that is half the work.
-//     Query tiles are launched last frame first, so that the longest ones start first.
+//     Query tiles are launched last frame first, so that the longest ones start first (TileOrder).
 //   * Cached keys are e4m3 codes. Three producer warps for K and three for V copy them into
 //     a staging buffer, expand them to f16 (one conversion per two codes, exact) and store them
 //     into the swizzled tile; the tensor core then works on f16 operands. A block's scale enters
@@ -351,7 +351,11 @@ __device__ __forceinline__ int q_row_to_f16(uint32_t tile, int row) {
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frames_kernel(const FramesFwdParams p) {
     using C = Cfg<D, CACHE>;
-    int pair = p.npairs - 1 - blockIdx.x, head = blockIdx.y, seq = blockIdx.z;
+    int pair, head, seq;
+    if (!CACHE) {
+        p.order.get(blockIdx.x, p.g.heads, pair, seq, head);
+        pair = p.npairs - 1 - pair;
+    }
     // cache: this CTA's number among those of the items that are cut, negative for a whole item
     const int over = CACHE ? static_cast<int>(blockIdx.x) - static_cast<int>(p.plan.whole) : -1;
     const int splits = over >= 0 ? p.plan.splits : 1;
@@ -1076,11 +1080,8 @@ int launch_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
         }
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
-    dim3 grid(p.npairs, g.heads, g.B * g.Ph * g.Pw);
-    if (CACHE) {
-        const long long items = static_cast<long long>(grid.x) * grid.y * grid.z;
-        grid = dim3(static_cast<unsigned>(p.plan.whole + (items - p.plan.whole) * p.plan.splits));
-    }
+    const long long items = static_cast<long long>(p.npairs) * g.heads * g.B * g.Ph * g.Pw;
+    const dim3 grid(static_cast<unsigned>(CACHE ? p.plan.whole + (items - p.plan.whole) * p.plan.splits : items));
     skiparse_attn_frames_kernel<D, CACHE><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !CACHE || p.plan.splits == 1) return static_cast<int>(e);
@@ -1145,6 +1146,7 @@ int launch_frames_fwd(FramesFwdParams p, const Geometry& g, void* stream) {
     p.dPairs.init(p.npairs);
     p.dHeads.init(g.heads);
     p.dSplits.init(p.plan.splits);
+    p.order.init(g.heads * g.B * g.Ph * g.Pw, p.npairs, g.heads);
     switch (g.d) {
         case 32: return launch_kind<32>(p, g, st);
         case 64: return launch_kind<64>(p, g, st);

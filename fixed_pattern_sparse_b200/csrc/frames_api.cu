@@ -165,6 +165,7 @@ int relbias_bwd(int dims, const void* q, const void* k, const void* v, const voi
     p.ND = w.ND;
     p.seqs = B * g.Ph * g.Pw;
     p.tiles = w.tiles;
+    p.order.init(heads * p.seqs, p.tiles, heads);
     p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
     p.scale_log2 = static_cast<float>(log2e_over_sqrt(d));
     p.wait_limit_ns = api::wait_limit_ns();
