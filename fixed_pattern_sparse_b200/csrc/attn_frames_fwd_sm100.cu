@@ -20,11 +20,12 @@
 //     a staging buffer, expand them to f16 (one conversion per two codes, exact) and store them
 //     into the swizzled tile; the tensor core then works on f16 operands. A block's scale enters
 //     as 2^(e - ref), ref the largest e among the keys this CTA reads, so that a single power
-//     of two for K (in the softmax's factor) and one for V (in the epilogue) are left: exact while
-//     a code times its factor keeps to f16's normal range, that is for blocks down to 2^-22 of
-//     the largest scale, and within 2^-34 of the largest magnitude below. Q's rows are scaled by a
-//     power of two each into f16, and P is kept as 2^7 p, so that f16 holds every p above 2^-31:
-//     P's rounding is 2^-11 instead of bf16's 2^-8.
+//     of two for K (in the softmax's factor) and one for V (in the epilogue) are left. Where the
+//     scales of these keys, masked ones included, spread beyond what that holds (kWideK, kWideV), the
+//     codes enter unscaled, K's scale multiplies the score and V's joins the exponent of its weight
+//     (wide_softmax): a block counts by its own values whatever the others' scales. Q's rows are
+//     scaled by a power of two each into f16, and P is kept as 2^7 p, so that f16 holds every p above
+//     2^-31: P's rounding is 2^-11 instead of bf16's 2^-8.
 //   * Few query tiles over a long cache leave SMs idle, and so does a last wave of few CTAs: the key
 //     range of these tiles is cut into parts, each CTA writes its normalised partial output and
 //     log-sum-exp in fp32, and a second kernel joins them.
@@ -54,6 +55,10 @@ constexpr int kProdWarp0 = 8;
 constexpr int kMaxSmem = 232448;      // 227 KB, the most a CTA may have
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by more than 2^8
 constexpr int kPParts = 2;            // P is released to the tensor core in two halves of the key tile
+// Largest spread, as a power of two, of the scales of a CTA's keys at which they enter the codes as f16
+// factors. K: a code's last bit is worth 2^-9 or more, f16's 2^-24: the product is exact. V: so is it, but weights
+// are off by up to 2^-32 of the row's largest, times 2^spread where that one's block is the smallest.
+constexpr int kWideK = 15, kWideV = 8;
 
 // The bias as part of S = Q K^T (bf16 keys): 16 more columns of Q and K. The frames of a CTA's queries, at
 // most five, are numbered; a query's row holds ones in the three columns of its frame, a key's row holds,
@@ -165,8 +170,8 @@ struct Cfg : TileGeom<D> {
     static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NBARS;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
     static constexpr int OFF_RANGE = OFF_ABORT + 4;  // first and last visible distance
-    static constexpr int OFF_REF = OFF_RANGE + 8;    // cache: largest scale bytes of K and V
-    static constexpr int SMEM_USED = OFF_REF + 8;
+    static constexpr int OFF_REF = OFF_RANGE + 8;    // cache: largest scale bytes of K and V, then smallest
+    static constexpr int SMEM_USED = OFF_REF + 16;
     // + slack for 1024-byte alignment where it fits (the kernel checks the slack it got); at
     // least 116 KB so that one CTA (and its 512 TMEM columns) owns an SM even for small d
     static constexpr int SMEM_BYTES =
@@ -348,6 +353,125 @@ __device__ __forceinline__ int q_row_to_f16(uint32_t tile, int row) {
     return up;
 }
 
+// The softmax of a query tile over keys whose scales spread (see kWideK): what it needs, as its caller has it.
+struct WideArgs {
+    int jbeg, jend, nF, step, first, tiles;  // key tile j of this query tile starts at jbeg + first + j * step
+    int tq, dmax, NBk;
+    uint32_t s_addr, o_addr, sfull, pfull;
+    float sl2;
+    const float* tab;
+    const uint8_t* k_scales;
+    const uint8_t* v_scales;
+    FastDiv dF;
+    FrameRing ring;
+    volatile int* abort;
+    uint64_t lim;
+};
+// S becomes the score plus the exponent of its value's block, whose running maximum m_w is the reference of the
+// weights; the row sum l and its reference m are taken from the scores alone. Returns m, l, m_w and whether
+// every wait ended. Such calls take 3 times as long (480p chunk 0.70 -> 2.2 ms, 720p frame 1.64 -> 4.9). A function
+// of its own: inlined, they take 2.3 to 2.5 times as long, but its presence costs the others 4 to 14 % (720p
+// frame 1.59 ms without it, 1.64 so, 1.67 to 1.81 inlined in several ways).
+template <int D>
+__device__ __noinline__ float4 wide_softmax(const WideArgs& a) {
+    float m_w = -INFINITY, m = -INFINITY, l = 0.f;
+    bool ok = true;
+    const auto bias_of = [&](int f) { return a.tab[clamp_dist(a.tq - a.ring.time(f), a.dmax) + a.dmax]; };
+    for (int j = 0; ok && j < a.tiles; ++j) {
+        const int j0 = a.jbeg + j * a.step + a.first;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(a.sfull, j & 1, a.abort, a.lim));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int g = 0; g < kBN / 16; ++g) {
+            const int jg = j0 + 16 * g;
+            uint32_t sv[16];
+            ptx::tmem_ld16(a.s_addr + 16 * g, sv);
+            ptx::tmem_wait_ld();
+            // scale of K, exponent of V and bias of key i, past the end those of the last
+            auto of_key = [&](int i, float& ks, float& ev, float& bias) {
+                i = min(i, a.jend - 1);
+                const int f = a.dF.div(i);
+                const long long at = static_cast<long long>(f) * a.NBk + (i - f * a.nF) / kCacheBlock;
+                const int kb = __ldg(a.k_scales + at), vb = __ldg(a.v_scales + at);
+                ks = kb == 255 ? NAN : exp2_int(kb - 127);
+                ev = vb == 255 ? NAN : static_cast<float>(vb - 127);
+                bias = bias_of(f);
+            };
+            float ev[16], top = m;
+            const int at0 = jg - a.dF.div(min(jg, a.jend - 1)) * a.nF;
+            if (jg + 16 <= a.jend && at0 + 16 <= a.nF && at0 % kCacheBlock + 16 <= kCacheBlock) {  // one block
+                float ks, bias;
+                of_key(jg, ks, ev[0], bias);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float x = bias == -INFINITY ? bias : fmaf(__uint_as_float(sv[e]) * a.sl2, ks, bias);
+                    sv[e] = __float_as_uint(x);
+                    ev[e] = ev[0];
+                    top = fmaxf(top, x);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float ks, bias;
+                    of_key(jg + e, ks, ev[e], bias);
+                    const float x = jg + e >= a.jend || bias == -INFINITY ? -INFINITY : fmaf(__uint_as_float(sv[e]) * a.sl2, ks, bias);
+                    sv[e] = __float_as_uint(x);
+                    top = fmaxf(top, x);
+                }
+            }
+            const float ref = top == -INFINITY ? 0.f : top;  // no key seen yet, or NaNs alone
+            l *= ptx::ex2_approx(m - ref);
+            m = top;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = __uint_as_float(sv[e]);
+                l += ptx::ex2_approx(x - ref);
+                sv[e] = __float_as_uint(x + ev[e]);
+                mx = fmaxf(mx, x + ev[e]);
+            }
+            ptx::tmem_st16(a.s_addr + 16 * g, sv);
+        }
+        ptx::tmem_wait_st();
+        float alpha = 1.f;
+        if (j == 0 || mx > m_w + kRescaleLog2) {
+            alpha = j == 0 ? 0.f : ptx::ex2_approx(m_w - mx);
+            m_w = mx;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int go = 0; go < D / 16; ++go) {
+                uint32_t ov[16];
+                const uint32_t o_addr = a.o_addr + 16 * go;
+                ptx::tmem_ld16(o_addr, ov);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                ptx::tmem_st16(o_addr, ov);
+            }
+        }
+        const float neg = kPShift - (m_w == -INFINITY ? 0.f : m_w);
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {  // the weights over columns that have been read
+            uint32_t sv[32], pk[16];
+            ptx::tmem_ld32(a.s_addr + 32 * g, sv);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                pk[e] = pack_f16x2(ptx::ex2_approx(__uint_as_float(sv[2 * e]) + neg),
+                                   ptx::ex2_approx(__uint_as_float(sv[2 * e + 1]) + neg));
+            ptx::tmem_st16(a.s_addr + 16 * g, pk);
+            if (g & 1) {
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(a.pfull + 8 * (g >> 1));
+            }
+        }
+    }
+    return make_float4(m, l, m_w, ok ? 1.f : 0.f);
+}
+
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frames_kernel(const FramesFwdParams p) {
     using C = Cfg<D, CACHE>;
@@ -432,6 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         ptx::mbar_init(bar(C::B_QF16), 2 * kBM);
         *abort = 0;
         refs[0] = refs[1] = 0;
+        refs[2] = refs[3] = 255;
         range[0] = dmax + 1;
         range[1] = -dmax - 1;
         ptx::fence_mbar_init();
@@ -483,29 +608,37 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
     const int first_tile = over >= 0 ? (over - p.dSplits.div(over) * splits) * per_split : 0;
     const int jbeg = f_lo * nF + first_tile * kBN;             // this CTA's first key
     const int nkv = max(0, min(per_split, nkv_all - first_tile));
-    // cache: the largest scale among the keys read. Codes enter the tensor core as f16 values
-    // code * 2^(e - ref), so that one power of two for K and one for V remain to be applied.
+    // cache: the largest and smallest scales among the keys read. Codes enter the tensor core as f16
+    // values code * 2^(e - ref), so that one power of two for K and one for V remain to be applied, or
+    // (wide) as they are.
     const long long sh = static_cast<long long>(seq) * p.g.heads + head;
     const uint8_t* k_scales = CACHE ? p.cache.ks + sh * p.cache.cap * p.cache.NBk : nullptr;
     const uint8_t* v_scales = CACHE ? p.cache.vs + sh * p.cache.cap * p.cache.NBk : nullptr;
     if (CACHE && nkv > 0) {
         const int s_lo = dF.div(jbeg), s_hi = dF.div(min(jbeg + nkv * kBN, jend) - 1);
         const int used = (nF + kCacheBlock - 1) / kCacheBlock, count = (s_hi - s_lo + 1) * used;
-        int kr = 0, vr = 0;
+        int kr = 0, vr = 0, kl = 255, vl = 255;
         for (int i = threadIdx.x; i < count; i += C::THREADS) {
             const long long at = static_cast<long long>(s_lo + i / used) * p.cache.NBk + i % used;
             const int kb = __ldg(k_scales + at), vb = __ldg(v_scales + at);
             kr = max(kr, kb == 255 ? 0 : kb);
             vr = max(vr, vb == 255 ? 0 : vb);
+            kl = min(kl, kb);
+            vl = min(vl, vb);
         }
         kr = __reduce_max_sync(0xffffffffu, kr);
         vr = __reduce_max_sync(0xffffffffu, vr);
+        kl = __reduce_min_sync(0xffffffffu, kl);
+        vl = __reduce_min_sync(0xffffffffu, vl);
         if (lane == 0) {
             atomicMax(&refs[0], kr);
             atomicMax(&refs[1], vr);
+            atomicMin(&refs[2], kl);
+            atomicMin(&refs[3], vl);
         }
         __syncthreads();
     }
+    const bool wide = CACHE && nkv > 0 && (refs[0] - refs[2] > kWideK || refs[1] - refs[3] > kWideV);
 
     if (CACHE) {
         // 512 threads start with 128 registers each; the softmax needs 168: 2 * 168 + 2 * 88 = 4 * 128
@@ -541,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
                 if (steps > 0) t.fetch(jbeg, jend, dF, nF, p.cache, p.status);
                 for (int j = 0; j < steps; ++j) {
                     cp_async_wait<0>();
-                    const bool one = t.all_ref(ref);
+                    const bool one = t.all_ref(ref) || wide;
                     if (!(ok = wait_empty(of_v, j))) break;
                     const uint32_t dst = slots + (j % C::KST) * C::TILE_BYTES;
                     if (one)
@@ -722,12 +855,113 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_Q), 0, abort, lim));
             if (ok) {
                 const int up = q_row_to_f16<D>(sbase + C::OFF_Q + qt * C::TILE_BYTES, row);
-                sl2 *= exp2_int(up + refs[0] - 127);
+                sl2 *= exp2_int(wide ? up : up + refs[0] - 127);
                 fence_proxy_async();
                 ptx::mbar_arrive(bar(C::B_QF16));
             }
         }
+        // The row's results from its reference and sum of weights (in log2), and the power of two left in V
+        auto finish = [&](bool ok, float m_run, float l_run, float v_scale) __attribute__((always_inline)) {
+            if (ok && (nkv == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_OFULL), 0, abort, lim)))) {
+                ptx::tc_fence_after();
+                // a row without a visible key: 0, and -inf for its log-sum-exp
+                if (!CACHE && m_run > BiasCols::FAR_LOG2) l_run = NAN;  // a bias that is not finite
+                float inv_l = l_run == 0.f ? 0.f : v_scale / l_run;
+                float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run) - (CACHE ? kPShift : 0.f);
+                float* other = reinterpret_cast<float*>(smem + C::OFF_K) + row;  // [d][128], over the finished K ring
+                float join = 0.f;  // weight of the other half's result
+                if (halves && nkv > 1) {
+                    // the second half's result and log-sum-exp go through shared memory to the first
+                    if (qt == 1) {
+#pragma unroll
+                        for (int g = 0; g < D / 32; ++g) {
+                            uint32_t ov[32];
+                            ptx::tmem_ld32(tmem + lane_base + o_col + 32 * g, ov);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) other[(32 * g + e) * kBM] = __uint_as_float(ov[e]) * inv_l;
+                        }
+                        tab[row] = l2;  // the softmax is done with the bias
+                    }
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    const float l2b = tab[row], top = fmaxf(l2, l2b) == -INFINITY ? 0.f : fmaxf(l2, l2b);
+                    const float wa = ptx::ex2_approx(l2 - top), wb = ptx::ex2_approx(l2b - top), sum = wa + wb;
+                    inv_l *= sum == 0.f ? 0.f : wa / sum;
+                    join = sum == 0.f ? 0.f : wb / sum;
+                    l2 = sum == 0.f ? -INFINITY : top + ptx::lg2_approx(sum);
+                }
+                const bool real = qi < n_q && !(halves && qt == 1) && row_ok(rows(qi), p.nrows, p.status);
+                const size_t grow = real ? static_cast<size_t>(rows(qi)) : 0;
+                const bool partial = CACHE && splits > 1;
+                size_t part = 0;  // its place
+                if (partial) {
+                    const int cut = p.dSplits.div(over);
+                    part = (static_cast<size_t>(cut) * (p.halves ? kBM : 2 * kBM) + (qi - q_first)) * splits + (over - cut * splits);
+                }
+                if (real) {
+                    if (partial)
+                        p.part_l[part] = l2;
+                    else if (p.lse)
+                        p.lse[grow] = l2 * 0.6931471805599453f;
+                }
+#pragma unroll
+                for (int g = 0; g < D / 32; ++g) {
+                    uint32_t ov[32];
+                    if (nkv > 0) {
+                        ptx::tmem_ld32(tmem + lane_base + o_col + 32 * g, ov);
+                        ptx::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = 0u;
+                    }
+                    if (halves && nkv > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), inv_l, join * other[(32 * g + e) * kBM]));
+                    }
+                    const float inv = halves && nkv > 1 ? 1.f : inv_l;
+                    if (partial) {
+                        if (real) {
+                            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * g);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
+                                                     __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
+                        }
+                    } else {
+                        auto store = [&](uint16_t* to, const uint32_t(&w)[16]) {
+                            uint4* dst = reinterpret_cast<uint4*>(to + grow * D);
+#pragma unroll
+                            for (int v4 = 0; v4 < 4; ++v4)
+                                dst[4 * g + v4] = make_uint4(w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2], w[4 * v4 + 3]);
+                        };
+                        uint32_t pkd[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pkd[e] = ptx::pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
+                        if (real) store(p.out, pkd);
+                        if (!CACHE && p.out_lo) {  // what the rounding took: exact in fp32, rounded once
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                pkd[e] = ptx::pack_bf16x2(
+                                    fmaf(__uint_as_float(ov[2 * e]), inv, -__uint_as_float(pkd[e] << 16)),
+                                    fmaf(__uint_as_float(ov[2 * e + 1]), inv, -__uint_as_float(pkd[e] & 0xffff0000u)));
+                            if (real) store(p.out_lo, pkd);
+                        }
+                    }
+                }
+            } else {
+                if (!*abort) record_abort(abort, p.status);
+                if (halves && nkv > 1) asm volatile("bar.arrive 1, 256;" ::: "memory");  // for warps that saw no failure
+            }
+        };
         const int tiles = halves ? (nkv - qt + 1) / 2 : nkv;  // of this query tile
+        if (CACHE && wide) {
+            const WideArgs wa{jbeg, jend, nF, halves ? 2 * kBN : kBN, halves ? qt * kBN : 0, tiles, tq, dmax, p.cache.NBk, s_addr, tmem + lane_base + o_col,
+                              sfull, bar(C::B_PFULL + kPParts * qt), sl2, tab, k_scales, v_scales, dF, ring, abort, lim};
+            const float4 r = wide_softmax<D>(wa);
+            finish(r.w != 0.f, r.x, r.y * 128.f, ptx::ex2_approx(r.z - r.x));
+        } else {
         int done = 0;
         if (!__any_sync(0xffffffffu, qi < n_q)) {
             // All 32 rows of the warp lie past the class's end: it leaves their S as it is (rows of P and
@@ -899,98 +1133,7 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
             }
             l_run = l_run * alpha + ((sum_a.x + sum_a.y) + (sum_b.x + sum_b.y));
         }
-        if (ok && (nkv == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar(C::B_OFULL), 0, abort, lim)))) {
-            ptx::tc_fence_after();
-            // a row without a visible key: 0, and -inf for its log-sum-exp
-            if (!CACHE && m_run > BiasCols::FAR_LOG2) l_run = NAN;  // a bias that is not finite
-            const float v_scale = CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f;
-            float inv_l = l_run == 0.f ? 0.f : v_scale / l_run;
-            float l2 = l_run == 0.f ? -INFINITY : m_run + ptx::lg2_approx(l_run) - (CACHE ? kPShift : 0.f);
-            float* other = reinterpret_cast<float*>(smem + C::OFF_K) + row;  // [d][128], over the finished K ring
-            float join = 0.f;  // weight of the other half's result
-            if (halves && nkv > 1) {
-                // the second half's result and log-sum-exp go through shared memory to the first
-                if (qt == 1) {
-#pragma unroll
-                    for (int g = 0; g < D / 32; ++g) {
-                        uint32_t ov[32];
-                        ptx::tmem_ld32(tmem + lane_base + o_col + 32 * g, ov);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) other[(32 * g + e) * kBM] = __uint_as_float(ov[e]) * inv_l;
-                    }
-                    tab[row] = l2;  // the softmax is done with the bias
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                const float l2b = tab[row], top = fmaxf(l2, l2b) == -INFINITY ? 0.f : fmaxf(l2, l2b);
-                const float wa = ptx::ex2_approx(l2 - top), wb = ptx::ex2_approx(l2b - top), sum = wa + wb;
-                inv_l *= sum == 0.f ? 0.f : wa / sum;
-                join = sum == 0.f ? 0.f : wb / sum;
-                l2 = sum == 0.f ? -INFINITY : top + ptx::lg2_approx(sum);
-            }
-            const bool real = qi < n_q && !(halves && qt == 1) && row_ok(rows(qi), p.nrows, p.status);
-            const size_t grow = real ? static_cast<size_t>(rows(qi)) : 0;
-            const bool partial = CACHE && splits > 1;
-            size_t part = 0;  // its place
-            if (partial) {
-                const int cut = p.dSplits.div(over);
-                part = (static_cast<size_t>(cut) * (p.halves ? kBM : 2 * kBM) + (qi - q_first)) * splits + (over - cut * splits);
-            }
-            if (real) {
-                if (partial)
-                    p.part_l[part] = l2;
-                else if (p.lse)
-                    p.lse[grow] = l2 * 0.6931471805599453f;
-            }
-#pragma unroll
-            for (int g = 0; g < D / 32; ++g) {
-                uint32_t ov[32];
-                if (nkv > 0) {
-                    ptx::tmem_ld32(tmem + lane_base + o_col + 32 * g, ov);
-                    ptx::tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] = 0u;
-                }
-                if (halves && nkv > 1) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), inv_l, join * other[(32 * g + e) * kBM]));
-                }
-                const float inv = halves && nkv > 1 ? 1.f : inv_l;
-                if (partial) {
-                    if (real) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * g);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
-                                                 __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
-                    }
-                } else {
-                    auto store = [&](uint16_t* to, const uint32_t(&w)[16]) {
-                        uint4* dst = reinterpret_cast<uint4*>(to + grow * D);
-#pragma unroll
-                        for (int v4 = 0; v4 < 4; ++v4)
-                            dst[4 * g + v4] = make_uint4(w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2], w[4 * v4 + 3]);
-                    };
-                    uint32_t pkd[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pkd[e] = ptx::pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
-                    if (real) store(p.out, pkd);
-                    if (!CACHE && p.out_lo) {  // what the rounding took: exact in fp32, rounded once
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            pkd[e] = ptx::pack_bf16x2(
-                                fmaf(__uint_as_float(ov[2 * e]), inv, -__uint_as_float(pkd[e] << 16)),
-                                fmaf(__uint_as_float(ov[2 * e + 1]), inv, -__uint_as_float(pkd[e] & 0xffff0000u)));
-                        if (real) store(p.out_lo, pkd);
-                    }
-                }
-            }
-        } else {
-            if (!*abort) record_abort(abort, p.status);
-            if (halves && nkv > 1) asm volatile("bar.arrive 1, 256;" ::: "memory");  // for warps that saw no failure
+        finish(ok, m_run, l_run, CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f);
         }
     }
 

@@ -376,7 +376,9 @@ SKIPARSE_API long long skiparse1d_cache_frame_tokens(int H, int W, int P);
  *   workspace : device memory of the caller, 256-byte aligned, of at least
  *             skiparse2d_attn_cached_workspace_bytes() bytes (0: may be NULL); as for the backward
  *             pass, one for each call that can run at the same time.
- * One kernel launch, or two where the keys of few queries are cut into parts and joined.
+ * One kernel launch, or two where the keys of few queries are cut into parts and joined. A block
+ * counts by its own values, whatever the scales of other blocks; with more than 32 queries a class, tiles of
+ * queries over keys whose scales differ by more than 2^15 (k) or 2^8 (v) take about three times as long.
  */
 SKIPARSE_API int skiparse2d_attn_cached(const void* q, const void* k_cache, const void* v_cache,
                                         const void* k_scale, const void* v_scale, const int* start,
