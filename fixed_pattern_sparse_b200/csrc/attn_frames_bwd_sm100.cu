@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) skiparse_frames_bwd_kernel(con
             }
             const long long at = load_row(rows(min(first + row, n_c - 1)), p.nrows, p.status);
             const float l = __ldg(p.lse + at) * kLog2E;
-            row_l2 = l < kLse2Low ? -kLse2Low : -l;
+            row_l2 = l == -INFINITY ? kNoKeys : -l;
             asm volatile("bar.sync 1, 256;" ::: "memory");
             row_d = d_of[row];
             if (h == 0 && row_real) p.nlse2[at] = row_l2;

@@ -12,10 +12,13 @@ namespace skiparse {
 
 // The bias of a pair of tokens depends on the distance of their frames, u = clamp(t_q - t_k,
 // -D, D): table[buckets[u + D]][head], the pair being masked where the bucket lies outside
-// [0, NB) or the entry is below kBiasMasked (so -inf and the lowest values of a type mask).
+// [0, NB) or the entry is at or below -65504 (so -inf, the lowest values of fp16, bf16 and fp32 and the
+// usual -1e9 mask). A row that sees such entries only would, if they counted, have scores and a
+// log-sum-exp whose fp32 rounding is too coarse for the backward pass to find the weights again and for
+// weights in f16 to keep in range: half a step, in log2, is 2^-8 at 65504 and 64 at 1e9.
 constexpr int kMaxDist = 255;                     // largest D
 constexpr int kMaxDistEntries = 2 * kMaxDist + 1;
-constexpr float kBiasMasked = -1e30f;
+constexpr float kBiasMasked = -65504.f;  // between bf16's -65280 and -65536
 
 struct FrameBias {
     const uint16_t* table;  // bf16 (NB, heads); nullptr: no bias and no mask
@@ -126,7 +129,7 @@ struct FramesBwdParams {
     const uint16_t* dout;
     const float* lse;
     float* delta;      // workspace (rows): D = rowsum(dO o (O + O_lo)), corrected, by the dQ kernel
-    float* nlse2;      // workspace (rows): -lse * log2(e), at most -kLse2Low, by the dQ kernel
+    float* nlse2;      // workspace (rows): -lse * log2(e), kNoKeys for a row without a visible key, by the dQ kernel
     float* part;       // workspace (heads, ND, seqs, tiles): sums of dS by frame distance
     uint16_t* dtable;  // bf16 (NB, heads)
     uint16_t* dq;
@@ -143,9 +146,9 @@ struct FramesBwdParams {
     long long nrows;
     int fault;
 };
-// log2-sum-exp that stands for a row without a visible key: its masked scores of -inf still
-// give exp2(-inf) = 0.
-constexpr float kLse2Low = -1e30f;
+// What stands for the -lse of a row without a visible key, whose lse is -inf: its masked scores of -inf
+// still give exp2(-inf) = 0.
+constexpr float kNoKeys = 1e30f;
 
 struct AppendParams {
     const uint16_t* k;

@@ -206,8 +206,8 @@ def skiparse2d_attn_relbias_fwd(q, k, v, table, buckets, P: int, mode: int, out=
 
     q, k, v, out: (B,T,H,W,heads,d) bf16; table: (num_buckets, heads) bf16; buckets:
     (2*max_distance+1) int32, the bucket of each frame distance t_q - t_k (frame_buckets makes the
-    usual map), a value outside [0, num_buckets) masking it (keys and values have to be finite there
-    too); lse: (B,T,H,W,heads) fp32, natural
+    usual map), a value outside [0, num_buckets) masking it, as an entry of the table at or below
+    -65504 does (keys and values have to be finite there too); lse: (B,T,H,W,heads) fp32, natural
     log; out_lo: an optional bf16 tensor like q that receives what rounding took from out, for a more
     exact backward pass. A row without a visible key gives 0 and lse -inf."""
     return _relbias_fwd(2, q, k, v, table, buckets, P, mode, out, lse, out_lo, stream)

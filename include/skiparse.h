@@ -276,9 +276,11 @@ SKIPARSE_API long long skiparse1d_rearranged_numel(int B, int T, int H, int W, i
  * g = buckets[u + D], the score is q.k/sqrt(d) + table[g][head].
  *   buckets : (2D+1) int32 on the device, 4-byte aligned. A value outside [0, num_buckets) masks
  *             the pair: -1 for u < 0 is the frame-causal mask, -1 for |u| >= w a window.
- *   table   : (num_buckets, heads) bf16, 2-byte aligned. An entry below -1e30 (-inf and the type's
- *             lowest value among them) masks like a bucket outside the range. Other entries keep within
- *             +-1e30; one that is +inf or NaN makes the rows that see it NaN.
+ *   table   : (num_buckets, heads) bf16, 2-byte aligned. An entry at or below -65504 (the lowest values
+ *             of fp16, bf16 and fp32, -1e9 and -inf among them) masks like a bucket outside the range.
+ *             Other entries keep to at most 65504; one that is +inf or NaN makes the rows that see it
+ *             NaN. Scores and their log-sum-exp are fp32: where those of a row lie near c, its weights and
+ *             gradients are off by up to 2^-20 |c| relative.
  * A query row without a visible key gives 0, lse -inf, and zero gradients. Masks act on scores:
  * keys and values at masked places have to be finite, as everywhere else.
  */
