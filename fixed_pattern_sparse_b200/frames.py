@@ -137,6 +137,8 @@ def _on(device: int, stream, call):
     what it allocates belongs to that stream."""
     if stream is None and device == torch.cuda.current_device():
         return call(_current_stream(device))
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"stream must be on cuda:{device}, got cuda:{stream.device_index}")
     with torch.cuda.device(device):
         if stream is None:
             return call(_current_stream(device))
