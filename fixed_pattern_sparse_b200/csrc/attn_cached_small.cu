@@ -94,18 +94,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
-    skiparse_cached_small_kernel(const FramesFwdParams p, int row_tiles) {
+    skiparse_cached_small_kernel(const FramesFwdParams p) {
     using C = SmallCfg<D, NQ>;
-    const int split = blockIdx.x / row_tiles, tile = blockIdx.x % row_tiles;
+    const int split = blockIdx.x;
     const int head = blockIdx.y;
     const int seq = blockIdx.z;
     ClassView cls;
     cls.init(p.g, seq);
     const int nF = cls.nF;
     const FastDiv dF = cls.dF;
-    const int n_q = p.g.T * nF;
-    const int q_first = tile * C::ROWS;
-    if (q_first >= n_q) return;
+    const int n_q = p.g.T * nF;  // at most C::ROWS
+    if (n_q == 0) return;
     const int start = p.cache.start[cls.b];
     if (start < 0 || start > kMaxStart) return;
     FrameRing ring;
@@ -134,7 +133,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
     }
     __syncthreads();
     int f_lo, f_hi;
-    ring.visible(start + dF.div(q_first), start + dF.div(min(q_first + C::ROWS, n_q) - 1), range[0], range[1], dmax, f_lo, f_hi);
+    ring.visible(start, start + p.g.T - 1, range[0], range[1], dmax, f_lo, f_hi);
     const int groups = f_hi >= f_lo ? ((f_hi - f_lo + 1) * nF + kKeys - 1) / kKeys : 0;
     const int per_split = (groups + p.plan.splits - 1) / p.plan.splits;
     const int jend = (f_hi + 1) * nF;
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
     int tq[NQ][2];
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
-        const int qi = min(q_first + 8 * t + g, n_q - 1);
+        const int qi = min(8 * t + g, n_q - 1);
         const uint16_t* src = p.q + static_cast<size_t>(load_row(rows(qi), p.nrows, p.status)) * D;
         uint32_t w[C::KL][C::KB / 2];
         uint32_t top = 0;
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             mul[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
-            tq[t][e] = start + dF.div(min(q_first + 8 * t + 2 * c + e, n_q - 1)) + dmax;
+            tq[t][e] = start + dF.div(min(8 * t + 2 * c + e, n_q - 1)) + dmax;
         }
     }
 
@@ -388,8 +387,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
     // each warp joins every fourth query; a lane takes D/32 columns
     constexpr int PER = D / 32;
     for (int row = warp; row < C::ROWS; row += kWarps) {
-        const int qi = q_first + row;
-        if (qi >= n_q) break;
+        if (row >= n_q) break;
         float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -409,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
         // a row without a visible key: 0, and -inf for its log-sum-exp
         const float scale = total == 0.f ? 0.f : ptx::ex2_approx(topv - top - kPShift) / total;
         const float l2 = total == 0.f ? -INFINITY : top + ptx::lg2_approx(total);
-        const long long grow = rows(qi);
+        const long long grow = rows(row);
         if (!row_ok(grow, p.nrows, p.status)) continue;
         if (p.plan.splits > 1) {
             float* dst = p.part_o + (grow * p.plan.splits + split) * D + lane * PER;
@@ -425,8 +423,8 @@ __global__ void __launch_bounds__(32 * kWarps, SmallCfg<D, NQ>::CTAS)
     }
 }
 
-// Tiles of 8 queries of a CTA for classes of n queries.
-int query_tiles(long long n) { return n >= 32 ? 4 : static_cast<int>((n + 7) / 8); }
+// Tiles of 8 queries of a CTA for classes of up to n queries, n <= kMaxRows.
+int query_tiles(int n) { return (n + 7) / 8; }
 
 template <int D, int NQ>
 int launch_small_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
@@ -441,15 +439,14 @@ int launch_small_d(const FramesFwdParams& p, const Geometry& g, cudaStream_t str
         if (e != cudaSuccess) return static_cast<int>(e);
         if (dev >= 0 && dev < 64) attr_done_dev[dev].store(1, std::memory_order_release);
     }
-    const int row_tiles = (g.T * max_class_tokens(g) + C::ROWS - 1) / C::ROWS;
-    const dim3 grid(static_cast<unsigned>(row_tiles) * p.plan.splits, g.heads, g.B * g.Ph * g.Pw);
-    skiparse_cached_small_kernel<D, NQ><<<grid, 32 * kWarps, C::SMEM_BYTES, stream>>>(p, row_tiles);
+    const dim3 grid(p.plan.splits, g.heads, g.B * g.Ph * g.Pw);
+    skiparse_cached_small_kernel<D, NQ><<<grid, 32 * kWarps, C::SMEM_BYTES, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
 }
 
 template <int D>
 int launch_small(const FramesFwdParams& p, const Geometry& g, cudaStream_t stream) {
-    switch (query_tiles(static_cast<long long>(g.T) * max_class_tokens(g))) {
+    switch (query_tiles(g.T * max_class_tokens(g))) {
         case 1: return launch_small_d<D, 1>(p, g, stream);
         case 2: return launch_small_d<D, 2>(p, g, stream);
         case 3: return launch_small_d<D, 3>(p, g, stream);
@@ -464,10 +461,9 @@ bool cached_small(const Geometry& g) { return static_cast<long long>(g.T) * max_
 // One wave of CTAs for up to 24 queries a class, two for more, of at least 512 keys each (measured:
 // more CTAs cost up to a quarter in small calls and gain nothing in large ones).
 int cached_small_splits(const Geometry& g, int cap) {
-    const long long n = static_cast<long long>(g.T) * max_class_tokens(g);
-    const int tiles = query_tiles(n), rows = 8 * tiles;
+    const int tiles = query_tiles(g.T * max_class_tokens(g));
     const long long keys = static_cast<long long>(cap) * max_class_tokens(g);
-    const long long ctas = (n + rows - 1) / rows * g.heads * g.B * g.Ph * g.Pw;
+    const long long ctas = static_cast<long long>(g.heads) * g.B * g.Ph * g.Pw;
     long long s = 148LL * (tiles == 2 || tiles == 3 ? 3 : 4) / ctas;
     if (s > keys / 512) s = keys / 512;
     return static_cast<int>(s < 1 ? 1 : s);
