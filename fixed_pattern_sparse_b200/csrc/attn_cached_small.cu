@@ -21,8 +21,8 @@
 // What bounds it: reading the cache, as long as a step's instructions (conversions foremost: 64 per
 // lane and step at d = 128, 4 clocks each) keep below the 180 clocks in which an SM's share
 // of HBM delivers its 4 KB. Measured, d = 128, one query a class, 192 classes and heads of 8000 keys (396 MB):
-// 88 us, 4.5 TB/s; d = 64, 12 to 20 queries a class, 64 of 4000 to 6700 keys (43 MB): 29 us, the latency of
-// 12 warps an SM.
+// 87 to 90 us, 4.4 to 4.5 TB/s; d = 64, 12 to 20 queries a class, 64 of 4000 to 6700 keys (43 MB): 29 to 32 us, the
+// latency of 12 warps an SM; d = 128, 20 queries a class, 48 of 58,000 keys (713 MB): 340 us, 2.1 TB/s.
 // Key groups are dealt to the warps of a CTA and, over long caches, to `splits` CTAs; warps join
 // through shared memory, CTAs through the join kernel of attn_frames_fwd_sm100.cu. A CTA has
 // 8, 16, 24 or 32 queries.
@@ -57,7 +57,9 @@ struct SmallCfg {
     static constexpr int VB = D / 8;                  // bytes of a lane's copy of a value
     static constexpr int KSTEPS = D / 16;
     static constexpr int MT = D / 16;                 // row tiles of O^T
-    static constexpr int CTAS = NQ == 4 ? 2 : NQ == 1 ? 4 : 3;  // per SM, by registers
+    // per SM, by registers: at d = 64 and 32 these counts spill nothing; at d = 128, three tiles (held to 168
+    // registers) spill 260 bytes a thread and four (255) 180, which other counts were not measured against
+    static constexpr int CTAS = NQ == 4 ? 2 : NQ == 1 ? 4 : 3;
 };
 
 template <int BYTES>

@@ -28,8 +28,8 @@
 //     Per score this costs one addition (half of one packed instruction).
 // Launches: dQ, which first takes D and L from its rows of out, dO and lse; dK/dV; dtable. (Row statistics
 // by a kernel of their own took the same at 480p and 7 us longer, of 183 and of 94, in small steps.)
-// What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): dQ 2.2 ms, dK and dV 3.3 ms,
-// 1.1 and 1.0 PFLOP/s. As in the unbiased backward pass, a key step waits on its chain of products and
+// What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): dQ 2.2 ms, dK and dV 3.3 ms at
+// 1965 MHz, 1.1 and 1.0 PFLOP/s; 2.4 and 3.6 in training steps back to back, under the power cap. As in the unbiased backward pass, a key step waits on its chain of products and
 // exponentials (2500 and 3600 clocks at d = 64, where the tensor core needs 770 and 1020 of them); the
 // frames add 7 % more streamed rows to dK and dV, and the sums of dS.
 #include <cuda_bf16.h>

@@ -14,7 +14,8 @@
 //     that hold a frame's border the bias comes as further columns of Q and K (bf16 keys, frames of
 //     64 tokens and more: BiasCols below), or by a pass over S in TMEM before the softmax.
 //   * The frames that some row of the CTA can see form a range, from the first and last visible
-//     distance of the table; only its keys are loaded. With a causal map that is half the work.
+//     distance of the table; only its keys are loaded. With a causal map that is half the work. (In a
+//     cache whose ring has turned over, frames do not lie in order of time: all are loaded, whatever the mask.)
 //     Query tiles are launched last frame first, so that the longest ones start first (TileOrder).
 //   * Cached keys are e4m3 codes. Three producer warps for K and three for V copy them into
 //     a staging buffer, expand them to f16 (one conversion per two codes, exact) and store them
@@ -35,9 +36,9 @@
 // Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB, staging (cache) 32 KB or bias
 // columns (bf16) 32 KB.
 // What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): 1.44 ms for 1.65 TFLOP, 1140
-// TFLOP/s. A key step of 256 queries takes 3100 to 3500 clocks against 2048 of tensor core and as many of
+// TFLOP/s, at 1965 MHz (1.6 in training steps back to back, under the power cap). A key step of 256 queries takes 3100 to 3500 clocks against 2048 of tensor core and as many of
 // exponentials; the rest is the dependency of the two tiles' softmax and products on each other. The
-// cache form adds the expansion of the codes: 0.65 ms for three frames over 24 (790 TFLOP/s).
+// cache form adds the expansion of the codes: 0.68 ms for three frames over 24 (760 TFLOP/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

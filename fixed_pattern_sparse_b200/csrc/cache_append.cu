@@ -7,13 +7,15 @@
 // the codes to the tensor cores as f16 without a second rounding. A block that holds an
 // infinity or a NaN is stored with a NaN scale.
 //
-// HBM-bound: 2 bytes read and 1 written per value. One CTA of 256 threads per block and head of
+// 2 bytes read and 1 written per value. One CTA of 256 threads per block and head of
 // K or V holds the block's 64 * d values in registers (16-byte loads; a token's d values are one
 // contiguous row of its head) between the maximum and the conversion, so the input is read once.
 // Heads are the fastest grid dimension: CTAs that run together read the neighbouring heads of
 // the same tokens, and write 64 * d contiguous bytes each. Eight CTAs an SM, which takes at most 32
-// registers a thread: at 36, one CTA fewer, both cases below took a third longer. Measured: a 720p frame
-// (111 MB moved) 18 us, 6.1 TB/s; two 480p clips of 21 frames (604 MB) 96 us, 6.3 TB/s.
+// registers a thread: at 36, one CTA fewer, both cases below took a third longer. Measured: two 480p clips of 21
+// frames (604 MB in and out) 96 to 104 us, bound by HBM as much as by its issue slots (83 % busy; 403 MB read from
+// DRAM, 141 written by its end); a 720p frame (111 MB) 18 to 20 us, of which DRAM has 74 MB read and 4 written (the
+// rest stays in L2): there the issue slots (65 to 69 % busy) and the launch bound it, not HBM.
 #include <cuda_runtime.h>
 
 #include "frames_common.cuh"

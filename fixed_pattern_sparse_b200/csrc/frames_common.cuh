@@ -45,7 +45,7 @@ struct FrameRing {
     __device__ __forceinline__ int time(int slot) const { return slot + base - (slot > newest ? cap : 0); }
     // Slots [f_lo, f_hi] that some query of frames [ta, tb] can see when the visible distances lie
     // in [dlo, dhi] (the end distances +-D stand for all beyond them; dlo > dhi: none is visible).
-    // All slots of a wrapped ring are taken.
+    // All slots of a wrapped ring are taken, hidden ones too: they lie in no order of time.
     __device__ __forceinline__ void visible(int ta, int tb, int dlo, int dhi, int D, int& f_lo, int& f_hi) const {
         f_lo = 0;
         f_hi = nframes - 1;
@@ -84,7 +84,8 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// 2^(byte - ref) as an f16 pair, byte <= ref: exact down to 2^-24, 0 below; NaN for byte 255.
+// 2^(byte - ref) as an f16 pair, byte <= ref: exact down to 2^-24, 0 below (where the codes enter unscaled and this
+// is not used); NaN for byte 255.
 __device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte, int ref) {
     const int down = ref - static_cast<int>(byte);
     uint32_t h = down <= 14 ? static_cast<uint32_t>(15 - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;

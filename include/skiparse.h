@@ -353,7 +353,8 @@ SKIPARSE_API long long skiparse1d_attn_relbias_bwd_workspace_bytes(int B, int T,
  * skiparse2d_cache_append quantises k and v, (B, T, H, W, heads, d) bf16, into their slots: a block's
  * scale is 2^e with the smallest whole e >= -110 for which its values fit +-448 * 2^e; a code is
  * x / 2^e rounded to nearest even. A block with an infinity or a NaN gets a NaN scale, and what
- * attends to it becomes NaN. Other writers of the cache keep to finite codes. T <= capacity.
+ * attends to it becomes NaN, as may rows that mask it (see above). Other writers of the cache keep to
+ * finite codes and to scales of 2^-110 and more. T <= capacity.
  * capacity * F <= 2^30.
  */
 SKIPARSE_API int skiparse2d_cache_append(const void* k, const void* v, const int* start, void* k_cache,
