@@ -60,7 +60,7 @@ def parity_map(D, masked):
     return torch.where(u % 2 == 0, 0, -1 if masked else 1).to(torch.int32).cuda()
 
 
-@pytest.mark.parametrize("spread", [4, 8, 9, 16, 24, 30, 60])
+@pytest.mark.parametrize("spread", [4, 8, 9, 14, 16, 24, 30, 60])
 @pytest.mark.parametrize("kind", ["v", "v_masked", "k", "k_and_v"])
 @pytest.mark.parametrize("call", CALLS, ids=lambda c: "x".join(map(str, c)))
 def test_frames_of_unequal_scale(fps, call, kind, spread):
