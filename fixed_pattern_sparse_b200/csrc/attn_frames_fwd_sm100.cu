@@ -35,10 +35,11 @@
 //     length of a CTA and doubles their number.
 // Shared memory at d = 128: Q 64 KB, K and V rings 64 KB each, table 2 KB, staging (cache) 32 KB or bias
 // columns (bf16) 32 KB.
-// What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): 1.44 ms for 1.65 TFLOP, 1140
-// TFLOP/s, at 1965 MHz (1.6 in training steps back to back, under the power cap). A key step of 256 queries takes 3100 to 3500 clocks against 2048 of tensor core and as many of
-// exponentials; the rest is the dependency of the two tiles' softmax and products on each other. The
-// cache form adds the expansion of the codes: 0.68 ms for three frames over 24 (760 TFLOP/s).
+// What bounds it, 480p (21 frames of 390 tokens a class, d = 128, 12 heads): 1.45 ms for 1.65 TFLOP, 1140
+// TFLOP/s, at 1965 MHz (1.6 in training steps back to back, under the power cap). A key step of 256
+// queries takes 3100 to 3500 clocks against 2048 of tensor core and as many of exponentials; the rest is
+// the dependency of the two tiles' softmax and products on each other. The cache form adds the expansion
+// of the codes: 0.68 ms for three frames over 24 (760 TFLOP/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -370,7 +371,8 @@ struct WideArgs {
 };
 // S becomes the score plus the exponent of its value's block, whose running maximum m_w is the reference of the
 // weights; the row sum l and its reference m are taken from the scores alone. Returns m, l, m_w and whether
-// every wait ended. Such calls take 3 times as long (480p chunk 0.70 -> 2.2 ms, 720p frame 1.64 -> 4.9). A function
+// every wait ended. Such calls take 3 times as long (480p chunk 0.70 -> 2.3 ms, 720p frame 1.65 -> 5.1; d = 64 and 32
+// twice: 333 -> 665 us, 288 -> 628). A function
 // of its own: inlined, they take 2.3 to 2.5 times as long, but its presence costs the others 4 to 14 % (720p
 // frame 1.59 ms without it, 1.64 so, 1.67 to 1.81 inlined in several ways).
 template <int D>
@@ -417,7 +419,8 @@ __device__ __noinline__ float4 wide_softmax(const WideArgs& a) {
                 for (int e = 0; e < 16; ++e) {
                     float ks, bias;
                     of_key(jg + e, ks, ev[e], bias);
-                    const float x = jg + e >= a.jend || bias == -INFINITY ? -INFINITY : fmaf(__uint_as_float(sv[e]) * a.sl2, ks, bias);
+                    const bool hidden = jg + e >= a.jend || bias == -INFINITY;
+                    const float x = hidden ? -INFINITY : fmaf(__uint_as_float(sv[e]) * a.sl2, ks, bias);
                     sv[e] = __float_as_uint(x);
                     top = fmaxf(top, x);
                 }
@@ -958,183 +961,184 @@ __global__ void __launch_bounds__(Cfg<D, CACHE>::THREADS, 1) skiparse_attn_frame
         };
         const int tiles = halves ? (nkv - qt + 1) / 2 : nkv;  // of this query tile
         if (CACHE && wide) {
-            const WideArgs wa{jbeg, jend, nF, halves ? 2 * kBN : kBN, halves ? qt * kBN : 0, tiles, tq, dmax, p.cache.NBk, s_addr, tmem + lane_base + o_col,
+            const WideArgs wa{jbeg, jend, nF, halves ? 2 * kBN : kBN, halves ? qt * kBN : 0, ok ? tiles : 0,
+                              tq, dmax, p.cache.NBk, s_addr, tmem + lane_base + o_col,
                               sfull, bar(C::B_PFULL + kPParts * qt), sl2, tab, k_scales, v_scales, dF, ring, abort, lim};
             const float4 r = wide_softmax<D>(wa);
-            finish(r.w != 0.f, r.x, r.y * 128.f, ptx::ex2_approx(r.z - r.x));
+            finish(ok && r.w != 0.f, r.x, r.y * 128.f, ptx::ex2_approx(r.z - r.x));  // l * 2^kPShift, as sums of stored P
         } else {
-        int done = 0;
-        if (!__any_sync(0xffffffffu, qi < n_q)) {
-            // All 32 rows of the warp lie past the class's end: it leaves their S as it is (rows of P and
-            // O do not mix) and only keeps the barriers going.
-            for (; ok && done < tiles; ++done) {
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(sfull, done & 1, abort, lim));
-                for (int h = 0; ok && h < kPParts; ++h) ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + h));
+            int done = 0;
+            if (!__any_sync(0xffffffffu, qi < n_q)) {
+                // All 32 rows of the warp lie past the class's end: it leaves their S as it is (rows of P and
+                // O do not mix) and only keeps the barriers going.
+                for (; ok && done < tiles; ++done) {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(sfull, done & 1, abort, lim));
+                    for (int h = 0; ok && h < kPParts; ++h) ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + h));
+                }
             }
-        }
-        for (int j = done; ok && j < tiles; ++j) {
-            // Every wait of a softmax warp is made uniform over the warp (a lane can see the abort
-            // flag while another sees the phase complete): the tcgen05.ld/st below are
-            // .sync.aligned and need all 32 lanes.
-            const int j0 = jbeg + (halves ? 2 * j + qt : j) * kBN;
-            const int f0 = dF.div(j0);
-            const int border = (f0 + 1) * nF - j0;  // tile column where the next frame starts
-            float off = !CACHE && cols ? 0.f : bias_of(f0), mul = sl2;  // scores are S * mul + off, in log2
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(sfull, j & 1, abort, lim))) {
-                ok = false;
-                break;
-            }
-            ptx::tc_fence_after();
-            // Whether a frame starts inside the tile, and with another bias (for some row of this warp; distances
-            // that share a bucket are common): d = 64 and 32, 40 and 64 frames, 910 -> 859 and 682 -> 620 us. At
-            // d = 128 the second question costs more than it saves (480p chunk 636 -> 698 us).
-            bool mixed = border < kBN && (CACHE ? p.bias.table != nullptr : !cols);
-            if (CACHE && D < 128 && mixed && border + nF >= kBN) mixed = __any_sync(0xffffffffu, bias_of(f0 + 1) != off);
-            if (mixed) {
-                // S becomes S * scale + bias in place, some columns at a
-                // time, before the softmax below reads the row. (Biases per 32 columns carried through
-                // the softmax instead cost the tiles without a border 18 %.)
-                if (nF >= 32) {  // at most one border in 32 columns
-                    int f = f0, next = border;  // column of this chunk where the next frame starts
+            for (int j = done; ok && j < tiles; ++j) {
+                // Every wait of a softmax warp is made uniform over the warp (a lane can see the abort
+                // flag while another sees the phase complete): the tcgen05.ld/st below are
+                // .sync.aligned and need all 32 lanes.
+                const int j0 = jbeg + (halves ? 2 * j + qt : j) * kBN;
+                const int f0 = dF.div(j0);
+                const int border = (f0 + 1) * nF - j0;  // tile column where the next frame starts
+                float off = !CACHE && cols ? 0.f : bias_of(f0), mul = sl2;  // scores are S * mul + off, in log2
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(sfull, j & 1, abort, lim))) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                // Whether a frame starts inside the tile, and with another bias (for some row of this warp; distances
+                // that share a bucket are common): d = 64 and 32, 40 and 64 frames, 910 -> 859 and 682 -> 620 us. At
+                // d = 128 the second question costs more than it saves (480p chunk 636 -> 698 us).
+                bool mixed = border < kBN && (CACHE ? p.bias.table != nullptr : !cols);
+                if (CACHE && D < 128 && mixed && border + nF >= kBN) mixed = __any_sync(0xffffffffu, bias_of(f0 + 1) != off);
+                if (mixed) {
+                    // S becomes S * scale + bias in place, some columns at a
+                    // time, before the softmax below reads the row. (Biases per 32 columns carried through
+                    // the softmax instead cost the tiles without a border 18 %.)
+                    if (nF >= 32) {  // at most one border in 32 columns
+                        int f = f0, next = border;  // column of this chunk where the next frame starts
 #pragma unroll 1
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t sv[32];
-                        ptx::tmem_ld32(s_addr + 32 * g, sv);
-                        ptx::tmem_wait_ld();
-                        if (next >= 32) {
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t sv[32];
+                            ptx::tmem_ld32(s_addr + 32 * g, sv);
+                            ptx::tmem_wait_ld();
+                            if (next >= 32) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {  // two columns per instruction
-                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
-                                                            make_float2(sl2, sl2), make_float2(off, off));
-                                sv[e] = __float_as_uint(y.x);
-                                sv[e + 1] = __float_as_uint(y.y);
+                                for (int e = 0; e < 32; e += 2) {  // two columns per instruction
+                                    const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                                                make_float2(sl2, sl2), make_float2(off, off));
+                                    sv[e] = __float_as_uint(y.x);
+                                    sv[e + 1] = __float_as_uint(y.y);
+                                }
+                            } else {
+                                const float o1 = bias_of(++f);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, e < next ? off : o1));
+                                off = o1;
+                                next += nF;
                             }
-                        } else {
-                            const float o1 = bias_of(++f);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, e < next ? off : o1));
-                            off = o1;
-                            next += nF;
+                            next -= 32;
+                            ptx::tmem_st16(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+                            ptx::tmem_st16(s_addr + 32 * g + 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
                         }
-                        next -= 32;
-                        ptx::tmem_st16(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
-                        ptx::tmem_st16(s_addr + 32 * g + 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
-                    }
-                } else {
-                    // Frames of fewer tokens: a lookup per score (columns past the last frame are masked
-                    // below). The width decides how the rest of this loop compiles: 16 columns make the
-                    // bf16 form 6 % faster than 32 at 480p, 32 the cache form 7 % faster than 16 at 720p.
-                    constexpr int WIDTH = CACHE ? 32 : 16;
-#pragma unroll 1
-                    for (int g = 0; g < kBN / WIDTH; ++g) {
-                        const int jg = j0 + WIDTH * g;
-                        uint32_t sv[WIDTH];
-                        if constexpr (WIDTH == 32)
-                            ptx::tmem_ld32(s_addr + WIDTH * g, sv);
-                        else
-                            ptx::tmem_ld16(s_addr + WIDTH * g, sv);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < WIDTH; ++e)
-                            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, bias_of(dF.div(jg + e))));
-#pragma unroll
-                        for (int w = 0; w < WIDTH; w += 16)
-                            ptx::tmem_st16(s_addr + WIDTH * g + w, *reinterpret_cast<uint32_t(*)[16]>(&sv[w]));
-                    }
-                }
-                ptx::tmem_wait_st();
-                off = 0.f;
-                mul = 1.f;
-            }
-            float sc[kBN];
-            {
-                uint32_t sv[kBN];
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    ptx::tmem_ld32(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * g]));
-                ptx::tmem_wait_ld();  // one wait for the whole 128-column row
-#pragma unroll
-                for (int e = 0; e < kBN; ++e) sc[e] = __uint_as_float(sv[e]);
-            }
-            if (j0 + kBN > jend) {
-                const int valid = jend - j0;
-#pragma unroll
-                for (int e = 0; e < kBN; ++e)
-                    if (e >= valid) sc[e] = -INFINITY;
-            }
-            // row max with 3-input max instructions, four independent chains
-            float mx0 = ptx::max3f(sc[0], sc[1], sc[2]), mx1 = ptx::max3f(sc[3], sc[4], sc[5]);
-            float mx2 = ptx::max3f(sc[6], sc[7], sc[8]), mx3 = ptx::max3f(sc[9], sc[10], sc[11]);
-#pragma unroll
-            for (int e = 12; e + 8 <= kBN; e += 8) {
-                mx0 = ptx::max3f(mx0, sc[e], sc[e + 1]);
-                mx1 = ptx::max3f(mx1, sc[e + 2], sc[e + 3]);
-                mx2 = ptx::max3f(mx2, sc[e + 4], sc[e + 5]);
-                mx3 = ptx::max3f(mx3, sc[e + 6], sc[e + 7]);
-            }
-            static_assert((kBN - 12) % 8 == 4, "tail of the max chains");
-            mx0 = ptx::max3f(mx0, sc[kBN - 4], sc[kBN - 3]);
-            mx1 = ptx::max3f(mx1, sc[kBN - 2], sc[kBN - 1]);
-            const float mx = fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), mul, off);
-            float alpha = 1.f;
-            if (j == 0 || mx > m_run + kRescaleLog2) {  // m_run = -inf: O and l are zero, alpha 0 keeps them
-                alpha = (j == 0) ? 0.f : ptx::ex2_approx(m_run - mx);
-                m_run = mx;
-            }
-            // P = 2^(S*scale*log2(e) + bias - m), written as bf16 pairs over the first 64 columns of
-            // S, in two halves released as they are stored. A row that has seen no key yet keeps
-            // the reference 0, so that its -inf scores give 0.
-            const float neg = off - (m_run < -BiasCols::FAR_LOG2 ? 0.f : m_run) + (CACHE ? kPShift : 0.f);
-            float2 sum_a = make_float2(0.f, 0.f), sum_b = sum_a;  // four short addition chains
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    // two columns per instruction (packed f32x2)
-                    const float2 x = __ffma2_rn(make_float2(sc[32 * g + 2 * e], sc[32 * g + 2 * e + 1]),
-                                                make_float2(mul, mul), make_float2(neg, neg));
-                    const float p0 = ptx::ex2_approx(x.x);
-                    const float p1 = ptx::ex2_approx(x.y);
-                    if (CACHE) {  // packed sums: 3 % faster here, 1 % slower in the bf16 form
-                        float2& sum = e & 1 ? sum_b : sum_a;
-                        sum = __fadd2_rn(sum, make_float2(p0, p1));
-                    } else if (e & 1) {
-                        sum_b.x += p0;
-                        sum_b.y += p1;
                     } else {
-                        sum_a.x += p0;
-                        sum_a.y += p1;
-                    }
-                    pk[e] = CACHE ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
-                }
-                ptx::tmem_st16(s_addr + 16 * g, pk);
-                if (g == 1 && j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // Rare: a row max grew by more than 2^8. This warp rescales its rows of O_qt
-                    // before releasing the first half of P, i.e. before this tile's P*V
-                    // accumulates into O_qt; O_qt was completed by the previous P*V (the commit
-                    // behind this tile's S covers it).
+                        // Frames of fewer tokens: a lookup per score (columns past the last frame are masked
+                        // below). The width decides how the rest of this loop compiles: 16 columns make the
+                        // bf16 form 6 % faster than 32 at 480p, 32 the cache form 7 % faster than 16 at 720p.
+                        constexpr int WIDTH = CACHE ? 32 : 16;
+#pragma unroll 1
+                        for (int g = 0; g < kBN / WIDTH; ++g) {
+                            const int jg = j0 + WIDTH * g;
+                            uint32_t sv[WIDTH];
+                            if constexpr (WIDTH == 32)
+                                ptx::tmem_ld32(s_addr + WIDTH * g, sv);
+                            else
+                                ptx::tmem_ld16(s_addr + WIDTH * g, sv);
+                            ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int go = 0; go < D / 16; ++go) {
-                        uint32_t ov[16];
-                        const uint32_t o_addr = tmem + lane_base + o_col + 16 * go;
-                        ptx::tmem_ld16(o_addr, ov);
-                        ptx::tmem_wait_ld();
+                            for (int e = 0; e < WIDTH; ++e)
+                                sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), sl2, bias_of(dF.div(jg + e))));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        ptx::tmem_st16(o_addr, ov);
+                            for (int w = 0; w < WIDTH; w += 16)
+                                ptx::tmem_st16(s_addr + WIDTH * g + w, *reinterpret_cast<uint32_t(*)[16]>(&sv[w]));
+                        }
                     }
-                }
-                if (g & 1) {
                     ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + (g >> 1)));
+                    off = 0.f;
+                    mul = 1.f;
                 }
+                float sc[kBN];
+                {
+                    uint32_t sv[kBN];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        ptx::tmem_ld32(s_addr + 32 * g, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * g]));
+                    ptx::tmem_wait_ld();  // one wait for the whole 128-column row
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e) sc[e] = __uint_as_float(sv[e]);
+                }
+                if (j0 + kBN > jend) {
+                    const int valid = jend - j0;
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e)
+                        if (e >= valid) sc[e] = -INFINITY;
+                }
+                // row max with 3-input max instructions, four independent chains
+                float mx0 = ptx::max3f(sc[0], sc[1], sc[2]), mx1 = ptx::max3f(sc[3], sc[4], sc[5]);
+                float mx2 = ptx::max3f(sc[6], sc[7], sc[8]), mx3 = ptx::max3f(sc[9], sc[10], sc[11]);
+#pragma unroll
+                for (int e = 12; e + 8 <= kBN; e += 8) {
+                    mx0 = ptx::max3f(mx0, sc[e], sc[e + 1]);
+                    mx1 = ptx::max3f(mx1, sc[e + 2], sc[e + 3]);
+                    mx2 = ptx::max3f(mx2, sc[e + 4], sc[e + 5]);
+                    mx3 = ptx::max3f(mx3, sc[e + 6], sc[e + 7]);
+                }
+                static_assert((kBN - 12) % 8 == 4, "tail of the max chains");
+                mx0 = ptx::max3f(mx0, sc[kBN - 4], sc[kBN - 3]);
+                mx1 = ptx::max3f(mx1, sc[kBN - 2], sc[kBN - 1]);
+                const float mx = fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), mul, off);
+                float alpha = 1.f;
+                if (j == 0 || mx > m_run + kRescaleLog2) {  // m_run = -inf: O and l are zero, alpha 0 keeps them
+                    alpha = (j == 0) ? 0.f : ptx::ex2_approx(m_run - mx);
+                    m_run = mx;
+                }
+                // P = 2^(S*scale*log2(e) + bias - m), written as bf16 pairs over the first 64 columns of
+                // S, in two halves released as they are stored. A row that has seen no key yet keeps
+                // the reference 0, so that its -inf scores give 0.
+                const float neg = off - (m_run < -BiasCols::FAR_LOG2 ? 0.f : m_run) + (CACHE ? kPShift : 0.f);
+                float2 sum_a = make_float2(0.f, 0.f), sum_b = sum_a;  // four short addition chains
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        // two columns per instruction (packed f32x2)
+                        const float2 x = __ffma2_rn(make_float2(sc[32 * g + 2 * e], sc[32 * g + 2 * e + 1]),
+                                                    make_float2(mul, mul), make_float2(neg, neg));
+                        const float p0 = ptx::ex2_approx(x.x);
+                        const float p1 = ptx::ex2_approx(x.y);
+                        if (CACHE) {  // packed sums: 3 % faster here, 1 % slower in the bf16 form
+                            float2& sum = e & 1 ? sum_b : sum_a;
+                            sum = __fadd2_rn(sum, make_float2(p0, p1));
+                        } else if (e & 1) {
+                            sum_b.x += p0;
+                            sum_b.y += p1;
+                        } else {
+                            sum_a.x += p0;
+                            sum_a.y += p1;
+                        }
+                        pk[e] = CACHE ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
+                    }
+                    ptx::tmem_st16(s_addr + 16 * g, pk);
+                    if (g == 1 && j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // Rare: a row max grew by more than 2^8. This warp rescales its rows of O_qt
+                        // before releasing the first half of P, i.e. before this tile's P*V
+                        // accumulates into O_qt; O_qt was completed by the previous P*V (the commit
+                        // behind this tile's S covers it).
+#pragma unroll
+                        for (int go = 0; go < D / 16; ++go) {
+                            uint32_t ov[16];
+                            const uint32_t o_addr = tmem + lane_base + o_col + 16 * go;
+                            ptx::tmem_ld16(o_addr, ov);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            ptx::tmem_st16(o_addr, ov);
+                        }
+                    }
+                    if (g & 1) {
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(bar(C::B_PFULL + kPParts * qt + (g >> 1)));
+                    }
+                }
+                l_run = l_run * alpha + ((sum_a.x + sum_a.y) + (sum_b.x + sum_b.y));
             }
-            l_run = l_run * alpha + ((sum_a.x + sum_a.y) + (sum_b.x + sum_b.y));
-        }
-        finish(ok, m_run, l_run, CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f);
+            finish(ok, m_run, l_run, CACHE && nkv > 0 ? exp2_int(refs[1] - 127) : 1.f);
         }
     }
 
